@@ -309,6 +309,180 @@ int moe_inv_rope_quant_per_head(const moe_rope_shape_t *shape, const void *x, co
                                 moe_stream_t stream);
 
 /*
+ * Attention side: a paged key/value cache, from request lengths to attention
+ * output (no counterpart on the pages: the steps between two MoE layers of a
+ * served decoder that come before moe_inv_rope_quant_per_head).
+ *   moe_page_plan        block tables, positions and cache slots of a batch
+ *   moe_rope_append      rotary embedding of q and k, k and v into their slots
+ *   moe_paged_attention  attention of the batch's new tokens over the cache
+ * Shared by the three:
+ *   - A batch is B requests.  Request b has cached[b] tokens in the cache and
+ *     brings fresh[b] more (0, 1 or a whole prompt).  The new tokens of all
+ *     requests are packed into one row axis: request b owns the rows
+ *     q_start[b] .. q_start[b+1]-1.  Row buffers may be longer than
+ *     q_start[B] (a captured graph's capacity); rows behind it are padding.
+ *   - A cache is num_pages pages of page_size tokens, k_cache and v_cache
+ *     [num_pages, page_size, n_kv_heads, head_dim] each, bf16 or E4M3 codes
+ *     (value = code * k_scale or v_scale).  page_stride is the distance between
+ *     two pages in elements (0: the pages are adjacent), so that K and V pages
+ *     may alternate in one buffer.  Position p of request b lives at offset
+ *     p % page_size of page block_table[b][p / page_size]; its slot is
+ *     page * page_size + offset.  num_pages * page_size is below 2^31;
+ *     addresses are computed in 64 bits.
+ *   - status: optional device int32 (may be NULL), set to MOE_ERR_DEVICE_CHECK
+ *     (if it was 0) when a kernel finds bad data, and left unchanged
+ *     otherwise.  No value in a device array makes a kernel access memory
+ *     outside the buffers described here.
+ *   - Two calls in flight at once may share inputs, but not outputs or a
+ *     workspace.
+ */
+
+/*
+ *   B           requests (1..4096)
+ *   max_tokens  rows of positions and slots (>= 0)
+ *   max_pages   columns of the block table (>= 1)
+ *   page_size   tokens per page (>= 1)
+ *   num_pages   pages of the cache (>= 1)
+ *   n_free      entries of free_pages (>= 0)
+ */
+typedef struct {
+    int32_t B, max_tokens, max_pages, page_size, num_pages, n_free;
+} moe_page_shape_t;
+
+/*
+ * Block table and slot map of a batch, from its lengths, in one launch.
+ *   cached [B], fresh [B] int32 in; free_pages [n_free] int32 in: page ids not
+ *   in use, taken from index *free_pos on (free_pos: device int32, NULL = 0).
+ *   block_table [B, max_pages] int32 in and out: request b's pages
+ *   ceil(cached/page_size) .. ceil((cached+fresh)/page_size)-1 are filled, in
+ *   request order, then in page order, with consecutive free pages; every
+ *   other entry is left as it is.  Out:
+ *     q_start   [B+1]         exclusive sums of fresh; last = tokens in all
+ *     kv_len    [B]           cached + fresh
+ *     positions [max_tokens]  cached[b] + i of request b's i-th new token
+ *     slots     [max_tokens]  that position's cache slot
+ *     free_next [1]           *free_pos + pages taken
+ *   Padding rows get position 0 and slot -1.  free_next may be NULL and must
+ *   not be free_pos.
+ *   Bad data sets the status, and: a request with a negative length or with
+ *   cached + fresh > max_pages * page_size counts as cached = fresh = 0; a page
+ *   that cannot be had (the free list has run out, or its id is outside
+ *   0..num_pages-1) is entered as -1, and tokens on such a page, or on an
+ *   entered page outside the cache, get slot -1; tokens beyond max_tokens have
+ *   no row (q_start still counts them).
+ * Errors: MOE_ERR_INVALID_ARG.  Asynchronous on `stream`.
+ */
+int moe_page_plan(const moe_page_shape_t *shape, const int32_t *cached, const int32_t *fresh,
+                  const int32_t *free_pages, const int32_t *free_pos, int32_t *block_table, int32_t *q_start,
+                  int32_t *kv_len, int32_t *positions, int32_t *slots, int32_t *free_next, int32_t *status,
+                  moe_stream_t stream);
+
+/*
+ *   num_tokens  rows (>= 0; 0 is a no-op)
+ *   n_heads, n_kv_heads  query heads and key/value heads (>= 1)
+ *   head_dim    64, 128 or 256
+ *   rot_dim     rotated elements per head, 0 (none) to head_dim: even for
+ *               interleaved pairs, a multiple of 16 for neox pairs
+ *   max_pos     rows of the rotary table
+ *   interleaved 0: pairs (i, i + rot_dim/2) ("neox"); 1: pairs (2i, 2i+1)
+ *   cache_dtype MOE_BF16 or MOE_E4M3
+ *   q_stride, k_stride, v_stride  elements from one token's heads to the next
+ *               token's, multiples of 8 (0: adjacent); a fused projection's
+ *               [tokens, n_heads + 2 n_kv_heads, head_dim] rows are read in place
+ *   page_stride elements from page to page, a multiple of 16 (0: adjacent)
+ *   k_scale, v_scale  static scales of an E4M3 cache (> 0; ignored for bf16)
+ */
+typedef struct {
+    int32_t num_tokens, n_heads, n_kv_heads, head_dim, rot_dim, max_pos, interleaved;
+    int32_t page_size, num_pages, cache_dtype;
+    int64_t q_stride, k_stride, v_stride, page_stride;
+    float k_scale, v_scale;
+} moe_append_shape_t;
+
+/*
+ * Rotary embedding fused with the cache write, one launch (the rotation that
+ * moe_inv_rope_quant_per_head takes back): every pair of a q or k head becomes
+ *   a' = a c - b s,  b' = b c + a s
+ * with c, s from row positions[t] of cos_sin (layout as there), fp32
+ * arithmetic, elements from rot_dim on unrotated.
+ *   q, k, v bf16 (16-byte aligned) in; positions, slots [num_tokens] int32 in;
+ *   cos_sin [max_pos, rot_dim] fp32 in (positions and cos_sin may be NULL when
+ *   rot_dim is 0); q_out [num_tokens, n_heads, head_dim] bf16 out (may be q
+ *   itself when q's rows are adjacent); k_cache, v_cache: the rotated k and the
+ *   unchanged v at their slots, bf16, or E4M3 codes of value / scale (IEEE
+ *   fp32 quotient, round to nearest even, saturated to +-448).
+ *   A token with slot -1 is padding: nothing of it is written, q_out included.
+ *   A slot below -1 or at or above num_pages * page_size, or a position outside
+ *   [0, max_pos) with rot_dim > 0, sets the status and the token is skipped in
+ *   the same way.  Slots of one call must differ: of two tokens with the same
+ *   slot either may be found there, in parts.
+ * Errors: MOE_ERR_INVALID_ARG (bad sizes, NULL or misaligned pointers),
+ * MOE_ERR_UNSUPPORTED (other head_dim or rot_dim).  Asynchronous on `stream`.
+ */
+int moe_rope_append(const moe_append_shape_t *shape, const void *q, const void *k, const void *v,
+                    const int32_t *positions, const int32_t *slots, const float *cos_sin, void *q_out,
+                    void *k_cache, void *v_cache, int32_t *status, moe_stream_t stream);
+
+/*
+ *   B           requests (1..4096)
+ *   num_tokens  rows of q and out (>= 0; 0 is a no-op)
+ *   n_heads, n_kv_heads  query heads and key/value heads (>= 1); n_heads is a
+ *               multiple of n_kv_heads, and query head h reads key/value head
+ *               h / (n_heads / n_kv_heads)
+ *   head_dim    64, 128 or 256
+ *   max_pages   columns of the block table; max_pages * page_size is at most 2^30
+ *   causal      1: the i-th of a request's n new tokens sees the keys
+ *               0 .. kv_len - n + i; 0: it sees all kv_len keys
+ *   max_q       the largest number of new tokens of one request as far as the
+ *               caller knows, 0 if unknown: it picks the kernels, and results
+ *               hold for every batch whatever it says
+ *   cache_dtype MOE_BF16 or MOE_E4M3
+ *   q_stride    elements from one token's heads to the next token's, a multiple
+ *               of 8 (0: adjacent)
+ *   page_stride elements from page to page, a multiple of 16 (0: adjacent)
+ *   scale       multiplies q . k before the softmax
+ *   k_scale, v_scale  static scales of an E4M3 cache (> 0; ignored for bf16)
+ */
+typedef struct {
+    int32_t B, num_tokens, n_heads, n_kv_heads, head_dim;
+    int32_t page_size, num_pages, max_pages, causal, max_q, cache_dtype;
+    int64_t q_stride, page_stride;
+    float scale, k_scale, v_scale;
+} moe_attn_shape_t;
+
+/* Bytes of workspace moe_paged_attention needs.  The workspace must be 256-byte
+ * aligned; its contents need no initialisation and are overwritten. */
+int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes);
+
+/*
+ * Attention of a batch's new tokens, whose keys and values are in the cache
+ * already, over the cache: for each new token t of request b and query head h
+ *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
+ * over the keys j the token sees.  Scores, the softmax's maximum and sum and
+ * the accumulation are fp32; p enters its product with v rounded to 16 bits.
+ *   q [num_tokens, n_heads, head_dim] bf16 (16-byte aligned), k_cache, v_cache
+ *   (16-byte aligned), block_table [B, max_pages], q_start [B+1], kv_len [B] in;
+ *   out [num_tokens, n_heads, head_dim] bf16 (16-byte aligned) out.
+ *   A token that sees no key (kv_len = 0, or fewer keys than new tokens) gets
+ *   zeros.  Rows behind q_start[B] are left as they are.
+ *   Cache positions at or beyond kv_len are never used, whatever they hold.
+ *   Within kv_len, a NaN or infinity in k or v may reach every new token of its
+ *   request, those that causal hides it from included.
+ *   Bad data sets the status, and: a kv_len below 0 or above max_pages *
+ *   page_size is clamped to that range; keys on a page outside the cache count
+ *   as k = v = 0; a request whose q_start range is not within [0, num_tokens]
+ *   or not ascending is skipped.
+ * The result of a call does not depend on what else runs or ran (the work split
+ * depends on the batch's lengths and the device alone; no atomics).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (other head_dim),
+ * MOE_ERR_WORKSPACE_TOO_SMALL.  A pipeline wait that runs out sets the status
+ * to MOE_ERR_TIMEOUT.  Asynchronous on `stream`.
+ */
+int moe_paged_attention(const moe_attn_shape_t *shape, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *block_table, const int32_t *q_start, const int32_t *kv_len, void *out,
+                        int32_t *status, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Self-test of the failure path (no counterpart on the pages): launches one
  * block whose two bounded pipeline waits run out, because nothing arrives on
  * their barriers.  The first gives up after the library's wait limit (2 s),

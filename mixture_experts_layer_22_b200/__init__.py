@@ -31,7 +31,8 @@ EXPORTS = ["moe_max_rows", "moe_workspace_size", "moe_route_topk", "moe_align_pe
            "moe_get_device_status", "moe_reset_device_status", "moe_status_string",
            "moe_last_launch_count", "moe_align_permute_noalloc", "moe_router_topk",
            "moe_fused_forward_router", "moe_selftest_wait_timeout", "moe_selftest_pair_abort",
-           "moe_inv_rope_quant_per_head"]
+           "moe_inv_rope_quant_per_head", "moe_page_plan", "moe_rope_append", "moe_attn_workspace_size",
+           "moe_paged_attention"]
 
 
 class MoeError(RuntimeError):
@@ -63,6 +64,31 @@ class RopeShape(C.Structure):
     def of(cls, rw, T: int | None = None) -> "RopeShape":
         return cls(num_tokens=rw.T if T is None else T, n_heads=rw.n_heads, head_dim=rw.head_dim,
                    rot_dim=rw.rot_dim, max_pos=rw.max_pos, interleaved=int(rw.interleaved))
+
+
+class PageShape(C.Structure):
+    """Mirror of moe_page_shape_t."""
+    _fields_ = [("B", C.c_int32), ("max_tokens", C.c_int32), ("max_pages", C.c_int32),
+                ("page_size", C.c_int32), ("num_pages", C.c_int32), ("n_free", C.c_int32)]
+
+
+class AppendShape(C.Structure):
+    """Mirror of moe_append_shape_t."""
+    _fields_ = [("num_tokens", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("max_pos", C.c_int32),
+                ("interleaved", C.c_int32), ("page_size", C.c_int32), ("num_pages", C.c_int32),
+                ("cache_dtype", C.c_int32), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("page_stride", C.c_int64), ("k_scale", C.c_float),
+                ("v_scale", C.c_float)]
+
+
+class AttnShape(C.Structure):
+    """Mirror of moe_attn_shape_t."""
+    _fields_ = [("B", C.c_int32), ("num_tokens", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("page_size", C.c_int32), ("num_pages", C.c_int32),
+                ("max_pages", C.c_int32), ("causal", C.c_int32), ("max_q", C.c_int32), ("cache_dtype", C.c_int32),
+                ("q_stride", C.c_int64), ("page_stride", C.c_int64), ("scale", C.c_float),
+                ("k_scale", C.c_float), ("v_scale", C.c_float)]
 
 
 _lib = None
@@ -97,6 +123,10 @@ def lib() -> C.CDLL:
             "moe_selftest_wait_timeout": [P, P, P],
             "moe_selftest_pair_abort": [S, P, P, P, P, P, C.c_size_t, P],
             "moe_inv_rope_quant_per_head": [C.POINTER(RopeShape), P, P, P, P, P, P, P],
+            "moe_page_plan": [C.POINTER(PageShape), P, P, P, P, P, P, P, P, P, P, P, P],
+            "moe_rope_append": [C.POINTER(AppendShape), P, P, P, P, P, P, P, P, P, P, P],
+            "moe_attn_workspace_size": [C.POINTER(AttnShape), C.POINTER(C.c_size_t)],
+            "moe_paged_attention": [C.POINTER(AttnShape), P, P, P, P, P, P, P, P, P, C.c_size_t, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -221,6 +251,105 @@ def inv_rope_quant(shape, x, positions, cos_sin, q, scales, status=None, stream=
     _check(lib().moe_inv_rope_quant_per_head(C.byref(shape), _ptr(x), _ptr(positions), _ptr(cos_sin), _ptr(q),
                                              _ptr(scales), _ptr(status), _stream(stream)),
            "moe_inv_rope_quant_per_head")
+
+
+def _dense(t, dtype, shape, what):
+    """Device address of a dense tensor of exactly this type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: dense device tensor {shape} {dtype} expected, got {tuple(t.shape)} {t.dtype} strides "
+                         f"{t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, n, heads, dim, stride, what):
+    """Device address of [n, heads, dim] bf16 rows `stride` elements apart (0: adjacent)."""
+    at = t.stride()
+    if (t.dtype != torch.bfloat16 or t.shape != (n, heads, dim) or not t.is_cuda or at[2] != 1 or
+            (heads > 1 and at[1] != dim) or (n > 1 and at[0] != (stride or heads * dim))):
+        raise ValueError(f"{what}: bf16 device tensor {(n, heads, dim)} with rows {stride or heads * dim} elements "
+                         f"apart expected, got {tuple(t.shape)} {t.dtype} strides {at} on {t.device}")
+    return t.data_ptr()
+
+
+def _cache(t, s, what):
+    """Device address of a cache [num_pages, page_size, n_kv_heads, head_dim]."""
+    row = s.n_kv_heads * s.head_dim
+    page = s.page_stride or s.page_size * row
+    at = t.stride()
+    if (t.dtype not in _CACHE_DTYPES[s.cache_dtype] or not t.is_cuda or
+            t.shape != (s.num_pages, s.page_size, s.n_kv_heads, s.head_dim) or at[3] != 1 or
+            (s.n_kv_heads > 1 and at[2] != s.head_dim) or (s.page_size > 1 and at[1] != row) or
+            (s.num_pages > 1 and at[0] != page)):
+        raise ValueError(f"{what}: device cache {(s.num_pages, s.page_size, s.n_kv_heads, s.head_dim)} with pages {page} "
+                         f"elements apart expected, got {tuple(t.shape)} {t.dtype} strides {at} on {t.device}")
+    return t.data_ptr()
+
+
+_CACHE_DTYPES = {BF16: (torch.bfloat16,), E4M3: (torch.uint8, torch.float8_e4m3fn)}
+_I32 = torch.int32
+
+
+def _word(t, what):
+    return None if t is None else _dense(t, _I32, (1,), what)
+
+
+def _same_device(*tensors):
+    """The calls launch on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def page_plan(shape, cached, fresh, free_pages, block_table, q_start, kv_len, positions, slots, free_next=None,
+              free_pos=None, status=None, stream=None):
+    """Block table entries, row ranges, positions and cache slots of a batch,
+    from its lengths (one launch)."""
+    s = shape
+    _same_device(cached, fresh, free_pages, block_table, q_start, kv_len, positions, slots, free_next, free_pos, status)
+    _check(lib().moe_page_plan(
+        C.byref(s), _dense(cached, _I32, (s.B,), "cached"), _dense(fresh, _I32, (s.B,), "fresh"),
+        _dense(free_pages, _I32, (s.n_free,), "free_pages"), _word(free_pos, "free_pos"),
+        _dense(block_table, _I32, (s.B, s.max_pages), "block_table"), _dense(q_start, _I32, (s.B + 1,), "q_start"),
+        _dense(kv_len, _I32, (s.B,), "kv_len"), _dense(positions, _I32, (s.max_tokens,), "positions"),
+        _dense(slots, _I32, (s.max_tokens,), "slots"), _word(free_next, "free_next"), _word(status, "status"),
+        _stream(stream)), "moe_page_plan")
+
+
+def rope_append(shape, q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache, status=None, stream=None):
+    """Rotary embedding of q and k, and k and v into their cache slots (one launch)."""
+    s = shape
+    n = s.num_tokens
+    _same_device(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache, status)
+    _check(lib().moe_rope_append(
+        C.byref(s), _rows(q, n, s.n_heads, s.head_dim, s.q_stride, "q"),
+        _rows(k, n, s.n_kv_heads, s.head_dim, s.k_stride, "k"), _rows(v, n, s.n_kv_heads, s.head_dim, s.v_stride, "v"),
+        None if positions is None else _dense(positions, _I32, (n,), "positions"), _dense(slots, _I32, (n,), "slots"),
+        None if cos_sin is None else _dense(cos_sin, torch.float32, (s.max_pos, s.rot_dim), "cos_sin"),
+        _rows(q_out, n, s.n_heads, s.head_dim, 0, "q_out"), _cache(k_cache, s, "k_cache"), _cache(v_cache, s, "v_cache"),
+        _word(status, "status"), _stream(stream)), "moe_rope_append")
+
+
+def attn_workspace_size(shape: AttnShape) -> int:
+    v = C.c_size_t()
+    _check(lib().moe_attn_workspace_size(C.byref(shape), C.byref(v)), "moe_attn_workspace_size")
+    return v.value
+
+
+def attn_workspace(shape: AttnShape, device="cuda") -> torch.Tensor:
+    return torch.empty(attn_workspace_size(shape), dtype=torch.uint8, device=device)
+
+
+def paged_attention(shape, q, k_cache, v_cache, block_table, q_start, kv_len, out, ws, status=None, stream=None):
+    """Attention of a batch's new tokens over the paged cache that holds them."""
+    s = shape
+    _same_device(q, k_cache, v_cache, block_table, q_start, kv_len, out, ws, status)
+    _check(lib().moe_paged_attention(
+        C.byref(s), _rows(q, s.num_tokens, s.n_heads, s.head_dim, s.q_stride, "q"), _cache(k_cache, s, "k_cache"),
+        _cache(v_cache, s, "v_cache"), _dense(block_table, _I32, (s.B, s.max_pages), "block_table"),
+        _dense(q_start, _I32, (s.B + 1,), "q_start"), _dense(kv_len, _I32, (s.B,), "kv_len"),
+        _rows(out, s.num_tokens, s.n_heads, s.head_dim, 0, "out"), _word(status, "status"), _ptr(ws), ws.numel(),
+        _stream(stream)), "moe_paged_attention")
 
 
 def selftest_wait_timeout(ws, gave_up, stream=None):

@@ -1,0 +1,756 @@
+// paged_attention.cu - attention of a batch's new tokens over a paged cache
+// (moe_paged_attention): the kernel for few query rows per request and for
+// every layout the tensor-memory kernel does not take, the kernel that joins
+// partial results, and the entry point.
+//
+// o_i = sum_j p_ij v_j / sum_j p_ij with p_ij = 2^(s_ij - m_i), s = q.k scale
+// log2(e), in one pass over the keys with the running maximum m_i and sum: when
+// a block of keys raises m_i, what was summed so far is scaled by 2^(old - new).
+//
+// A decode step reads every key and value of its requests once and does 4 group
+// operations per element read, so HBM bounds it: at 64 requests of up to 8192
+// keys 1.08 GB.  What it takes is bytes in flight from the first moment to the
+// last on every SM (see paged_work.cuh for the division of the work): a ring of
+// kStages blocks of 64 keys filled by cp.async, 2 to 3 CTAs per SM, and a load
+// side that runs ahead of the compute side over the borders of items, so that
+// short sequences keep the ring full too.  Page ids are read two blocks ahead
+// and turned into row offsets one block ahead.
+//
+// Products run on mma.sync m16n8k16: the 16 rows of one are the query heads of
+// a group, which tcgen05's 128 rows would leave nearly empty, and at this
+// arithmetic intensity the tensor pipe idles either way.
+#include <atomic>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "paged_work.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ uint32_t attn_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+// d += a b, 16 x 8 x 16, in bf16 or (kHalf) fp16 with fp32 sums
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (kHalf)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t f16x2_of(float a, float b)
+{
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// two E4M3 codes (the low 16 bits) as two fp16 values, exactly
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes)
+{
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
+    return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Geometry of one kernel: kWM warps down the query rows (16 each), 4 / kWM
+// along the keys of a block.
+template <int kD, bool kE4m3, int kWM>
+struct AttnCfg {
+    static constexpr int kThreads = 128, kBlk = 64;
+    static constexpr int kWN = 4 / kWM, kRows = 16 * kWM, kKeys = kBlk / kWN;
+    static constexpr int kRowBytes = kD * (kE4m3 ? 1 : 2), kChunks = kRowBytes / 16;
+    static constexpr int kStage = 2 * kBlk * kRowBytes;
+    static constexpr int kStages = kRowBytes <= 128 ? 4 : 3;
+    static constexpr int kQ = kRows * kD * 2;
+    static constexpr int kMerge = kWN > 1 ? kRows * kD * 4 : 0;
+    static constexpr int kSmem = kStages * kStage + kQ + kMerge;
+    // bf16 cache, few rows: p goes into its product as two bf16 (high and
+    // low part), which costs tensor work that is idle here and leaves the
+    // output's own rounding the only one of 8 bits.  With many rows that work
+    // counts, and p is rounded once; for an E4M3 cache it is fp16 (11 bits).
+    static constexpr bool kSplitP = !kE4m3 && kWM == 1;
+    static constexpr bool kQReg = kD <= 128;
+};
+
+// 16-byte chunk c of row r, permuted so that the 8 rows an ldmatrix reads at one
+// chunk lie in 8 different bank groups
+template <int kChunks>
+__device__ __forceinline__ int chunk_of(int r, int c)
+{
+    return kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+}
+
+template <int kD, bool kE4m3, int kWM>
+__global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p)
+{
+    using C = AttnCfg<kD, kE4m3, kWM>;
+    constexpr int kBlk = C::kBlk, kRows = C::kRows, kChunks = C::kChunks, kRowBytes = C::kRowBytes, kStages = C::kStages;
+    constexpr int kKeys = C::kKeys, kWN = C::kWN;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_off[2][kBlk];         // element offset of each key's row, -1: none
+    __shared__ float s_inv[kRows];               // 1 / the row's factor in q (E4M3 cache)
+    __shared__ float s_m[4][16], s_l[4][16];
+    const uint32_t ring = attn_smem(smem);
+    uint8_t *s_q = smem + kStages * C::kStage;
+    float *s_merge = reinterpret_cast<float *>(s_q + C::kQ);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wm = warp / kWN, wn = warp % kWN;
+
+    Split<128, kRows, kBlk> split;
+    Cursor<kRows, kBlk> cur;                     // the compute side
+    const long long n_blocks = split.init(p, cur);
+    if (n_blocks == 0) {
+        if (tid == 0) p.desc[blockIdx.x].parts = 0;
+        grid_dep_launch();
+        return;
+    }
+    grid_dep_launch();
+
+    // ---- load side: warps 0 and 1, a lane per key of a block ----
+    Cursor<kRows, kBlk> ld = cur;
+    long long ld_left = n_blocks;                // blocks whose page id is still to be read
+    int id_key = 0, id_page = 0, id_kvh = 0;     // the last id read: its key, page and head
+    bool id_in = false;
+    bool bad = false;
+    auto read_id = [&]() {                       // page id of the next block's key
+        if (ld_left > 0) {
+            id_key = ld.blk * kBlk + tid;
+            id_in = id_key < ld.r.kv;
+            id_kvh = ld.kvh;
+            id_page = id_in ? __ldg(p.table + static_cast<long long>(ld.b) * p.max_pages + id_key / p.page_size) : 0;
+            if (--ld_left > 0 && ++ld.blk == ld.nblk) ld.next_item(p);
+        } else {
+            id_in = false;
+        }
+    };
+    auto put_off = [&](int buf) {                // the id just read becomes an offset
+        long long off = -1;
+        if (id_in) {
+            if (id_page >= 0 && id_page < p.num_pages)
+                off = id_page * p.page_stride + (static_cast<long long>(id_key % p.page_size) * p.n_kv + id_kvh) * kD;
+            else
+                bad = true;
+        }
+        s_off[buf][tid] = off;
+    };
+    constexpr int esz = kE4m3 ? 1 : 2;
+    auto issue = [&](int stage, int buf) {       // all threads: copy one block's rows
+        const uint32_t dst = ring + stage * C::kStage;
+        constexpr int kPer = kBlk * kChunks / 128;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int x = tid + i * 128, r = x / kChunks, c = x % kChunks;
+            const long long off = s_off[buf][r];
+            const long long at = (off < 0 ? 0 : off * esz) + c * 16;
+            const uint32_t d = dst + r * kRowBytes + chunk_of<kChunks>(r, c) * 16;
+            cp_async16(d, static_cast<const uint8_t *>(p.k_cache) + at, off >= 0);
+            cp_async16(d + kBlk * kRowBytes, static_cast<const uint8_t *>(p.v_cache) + at, off >= 0);
+        }
+    };
+
+    if (warp < 2) {
+        read_id();
+        put_off(0);
+        read_id();
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {      // block i's offsets are in buffer i & 1
+        if (i < n_blocks) issue(i, i & 1);
+        cp_async_commit();
+        if (warp < 2) {
+            put_off((i + 1) & 1);
+            read_id();
+        }
+        __syncthreads();
+    }
+
+    // ---- compute side ----
+    float o[kD / 8][4];
+    float m[2], l[2];
+    uint32_t qf[C::kQReg ? kD / 16 : 1][4];
+    int lim[2];
+    float mult[2];
+    const int r_lo = 16 * wm + (lane >> 2), cq = lane & 3;
+    bool fresh_item = true;
+    long long item_from = 0;                     // where in this CTA's range the item starts
+    bool continued = cur.blk > 0;
+    const uint32_t sq = attn_smem(s_q);
+    auto load_qf = [&](uint32_t (&f)[4], int ks) {
+        const int r = 16 * wm + (lane & 15), c = 2 * ks + (lane >> 4);
+        ldsm4(f, sq + r * (kD * 2) + (c ^ (r & 7)) * 16);
+    };
+
+    for (long long it = 0; it < n_blocks; ++it) {
+        cp_async_wait<kStages - 2>();
+        if (fresh_item) {
+            // the item's query rows into shared memory.  For an E4M3 cache they
+            // become fp16 times a power of two that brings the row's largest
+            // magnitude to [2^14, 2^15): exact but for elements below 2^-28 of it,
+            // and the row's columns are permuted within 16 to the order in which
+            // ldmatrix delivers a row of bytes.
+            constexpr int kTpr = 128 / kRows, kCpt = kD / 8 / kTpr;   // threads per row, chunks per thread
+            const int r = tid / kTpr, part = tid % kTpr;
+            const int rows = cur.rows(p);
+            const int grow = cur.row0() + r;
+            const int tok = grow / p.group;
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                       static_cast<long long>(cur.r.qs + tok) * p.q_stride +
+                                       static_cast<long long>(cur.kvh * p.group + grow % p.group) * kD;
+            uint4 w[kCpt];
+#pragma unroll
+            for (int i = 0; i < kCpt; ++i)
+                w[i] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src) + part + i * kTpr) : make_uint4(0, 0, 0, 0);
+            if constexpr (kE4m3) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kCpt; ++i) {
+                    const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(ww[j] << 16)), fabsf(__uint_as_float(ww[j] & 0xFFFF0000u))));
+                }
+#pragma unroll
+                for (int o2 = kTpr / 2; o2 > 0; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
+                // the exponent field of a normal amax; 0 and subnormals as 2^-126
+                const int e = max(1, static_cast<int>(__float_as_uint(amax) >> 23)) - 127;
+                const int up = e == 128 ? 0 : min(126, 14 - e);
+                const float f = __int_as_float((127 + up) << 23);
+                if (part == 0) s_inv[r] = __int_as_float((127 - up) << 23);
+#pragma unroll
+                for (int i = 0; i < kCpt; ++i) {
+                    const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    const int c8 = part + i * kTpr;       // elements 8 c8 .. 8 c8 + 7
+                    // d = 16 ks + 4 c + {0, 1} -> column 2 c + {0, 1}, + {2, 3} -> 8 + 2 c + {0, 1}
+                    const int ks = c8 >> 1, c0 = (c8 & 1) * 2;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t h = f16x2_of(__uint_as_float(ww[j] << 16) * f, __uint_as_float(ww[j] & 0xFFFF0000u) * f);
+                        const int col = 2 * (c0 + (j >> 1)), chunk = 2 * ks + (j & 1);
+                        *reinterpret_cast<uint32_t *>(s_q + r * (kD * 2) + (chunk ^ (r & 7)) * 16 + col * 2) = h;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kCpt; ++i) {
+                    const int c = part + i * kTpr;
+                    *reinterpret_cast<uint4 *>(s_q + r * (kD * 2) + (c ^ (r & 7)) * 16) = w[i];
+                }
+            }
+        }
+        __syncthreads();
+        // block it has landed, block it - 1 has been read by every warp
+        {
+            const long long nx = it + kStages - 1;
+            if (nx < n_blocks) issue(static_cast<int>(nx % kStages), static_cast<int>(nx & 1));
+            cp_async_commit();
+            if (warp < 2) {
+                put_off(static_cast<int>((nx + 1) & 1));
+                read_id();
+            }
+        }
+        if (fresh_item) {
+#pragma unroll
+            for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = r_lo + 8 * h;
+                lim[h] = r < cur.rows(p) ? row_limit(p, cur.r, cur.row0() + r) : 0;
+                mult[h] = p.scale_log2 * (kE4m3 ? s_inv[r] : 1.0f);
+            }
+            if constexpr (C::kQReg) {
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks) load_qf(qf[ks], ks);
+            }
+            fresh_item = false;
+        }
+        const uint32_t kst = ring + static_cast<int>(it % kStages) * C::kStage, vst = kst + kBlk * kRowBytes;
+
+        // scores of the warp's rows and keys
+        float s[kKeys / 8][4];
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+        if constexpr (!kE4m3) {
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                if constexpr (!C::kQReg) load_qf(qf[0], ks);
+                const uint32_t (&a)[4] = qf[C::kQReg ? ks : 0];
+#pragma unroll
+                for (int np = 0; np < kKeys / 16; ++np) {
+                    const int r = wn * kKeys + np * 16 + (lane & 7) + ((lane >> 4) << 3), c = 2 * ks + ((lane >> 3) & 1);
+                    uint32_t b[4];
+                    ldsm4(b, kst + r * kRowBytes + chunk_of<kChunks>(r, c) * 16);
+                    mma16816<false>(s[2 * np], a, b[0], b[1]);
+                    mma16816<false>(s[2 * np + 1], a, b[2], b[3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k2 = 0; k2 < kD / 32; ++k2) {
+#pragma unroll
+                for (int np = 0; np < kKeys / 16; ++np) {
+                    // matrices: keys 0-7 and 8-15 at chunk 2 k2, then at 2 k2 + 1
+                    const int r = wn * kKeys + np * 16 + (lane & 15), c = 2 * k2 + (lane >> 4);
+                    uint32_t b[4];
+                    ldsm4(b, kst + r * kRowBytes + chunk_of<kChunks>(r, c) * 16);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        if constexpr (!C::kQReg) load_qf(qf[0], 2 * k2 + kk);
+                        const uint32_t (&a)[4] = qf[C::kQReg ? 2 * k2 + kk : 0];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = b[2 * kk + h];
+                            mma16816<true>(s[2 * np + h], a, f16x2_of_e4m3(x & 0xFFFFu), f16x2_of_e4m3(x >> 16));
+                        }
+                    }
+                }
+            }
+        }
+        // mask, running maximum, p
+        const int key0 = cur.blk * kBlk + wn * kKeys + 2 * cq;
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float t = key0 + 8 * i + (e & 1) < lim[e >> 1] ? s[i][e] * mult[e >> 1] : -INFINITY;
+                s[i][e] = t;
+                top[e >> 1] = fmaxf(top[e >> 1], t);
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+            const float mn = fmaxf(m[h], top[h]);
+            const float base = mn == -INFINITY ? 0.0f : mn;      // a row that has seen nothing yet
+            const float alpha = exp2_fast(m[h] - base);
+            m[h] = mn;
+            l[h] *= alpha;
+#pragma unroll
+            for (int i = 0; i < kKeys / 8; ++i)
+#pragma unroll
+                for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                    s[i][e] = exp2_fast(s[i][e] - base);
+                    l[h] += s[i][e];
+                }
+            if (alpha != 1.0f) {
+#pragma unroll
+                for (int i = 0; i < kD / 8; ++i) {
+                    o[i][2 * h] *= alpha;
+                    o[i][2 * h + 1] *= alpha;
+                }
+            }
+        }
+        // o += p v
+#pragma unroll
+        for (int kt = 0; kt < kKeys / 16; ++kt) {
+            uint32_t ph[4], pl[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = s[2 * kt + (j >> 1)][2 * (j & 1)], b = s[2 * kt + (j >> 1)][2 * (j & 1) + 1];
+                if constexpr (kE4m3) {
+                    ph[j] = f16x2_of(a, b);
+                } else {
+                    ph[j] = bf16x2_of(a, b);
+                    if constexpr (C::kSplitP)
+                        pl[j] = bf16x2_of(a - __uint_as_float(ph[j] << 16), b - __uint_as_float(ph[j] & 0xFFFF0000u));
+                }
+            }
+            const int r = wn * kKeys + kt * 16 + (lane & 15);
+#pragma unroll
+            for (int dp = 0; dp < kChunks / 2; ++dp) {
+                const int c = 2 * dp + (lane >> 4);
+                uint32_t b[4];
+                ldsm4_t(b, vst + r * kRowBytes + chunk_of<kChunks>(r, c) * 16);
+                if constexpr (!kE4m3) {
+                    mma16816<false>(o[2 * dp], ph, b[0], b[1]);
+                    mma16816<false>(o[2 * dp + 1], ph, b[2], b[3]);
+                    if constexpr (C::kSplitP) {
+                        mma16816<false>(o[2 * dp], pl, b[0], b[1]);
+                        mma16816<false>(o[2 * dp + 1], pl, b[2], b[3]);
+                    }
+                } else {
+                    // a 16-bit unit holds elements 2n and 2n + 1 of one key: tile
+                    // 2 ch takes the even ones of chunk ch, 2 ch + 1 the odd ones
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = __byte_perm(b[2 * h], 0, 0x3120), y = __byte_perm(b[2 * h + 1], 0, 0x3120);
+                        const int ch = 2 * dp + h;
+                        mma16816<true>(o[2 * ch], ph, f16x2_of_e4m3(x & 0xFFFFu), f16x2_of_e4m3(y & 0xFFFFu));
+                        mma16816<true>(o[2 * ch + 1], ph, f16x2_of_e4m3(x >> 16), f16x2_of_e4m3(y >> 16));
+                    }
+                }
+            }
+        }
+
+        // ---- the item's end, in this CTA ----
+        const bool last = cur.blk + 1 == cur.nblk;
+        if (last || it + 1 == n_blocks) {
+            const bool whole = last && !continued;
+            const int rows = cur.rows(p);
+            const long long slot = 2LL * blockIdx.x + (continued ? 0 : 1);
+            float *part = p.part + slot * (kRows * (kD + 2));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            }
+            // column of element e of the accumulator's tile i
+            auto col = [&](int i, int e) { return kE4m3 ? 16 * (i >> 1) + 4 * cq + 2 * e + (i & 1) : 8 * i + 2 * cq + e; };
+            if constexpr (kWN == 1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = r_lo + 8 * h;
+                    if (r < rows) {
+                        const int grow = cur.row0() + r;
+                        if (whole) {
+                            const float inv = l[h] > 0.0f ? p.v_scale / l[h] : l[h] == 0.0f ? 0.0f : l[h];
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                                 (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
+                                                  cur.kvh * p.group + grow % p.group) * kD;
+#pragma unroll
+                            for (int i = 0; i < kD / 8; ++i) {
+                                if constexpr (kE4m3) {
+                                    dst[col(i, 0)] = __float2bfloat16_rn(o[i][2 * h] * inv);
+                                    dst[col(i, 1)] = __float2bfloat16_rn(o[i][2 * h + 1] * inv);
+                                } else {
+                                    *reinterpret_cast<uint32_t *>(dst + col(i, 0)) = bf16x2_of(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kD / 8; ++i) {
+                                part[r * kD + col(i, 0)] = o[i][2 * h];
+                                part[r * kD + col(i, 1)] = o[i][2 * h + 1];
+                            }
+                            if (cq == 0) {
+                                part[kRows * kD + r] = m[h];
+                                part[kRows * kD + kRows + r] = l[h];
+                            }
+                        }
+                    }
+                }
+            } else {
+                // the warps hold different keys of the same rows: to one maximum,
+                // then summed in warp order
+                if (cq == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s_m[warp][r_lo + 8 * h] = m[h];
+                        s_l[warp][r_lo + 8 * h] = l[h];
+                    }
+                }
+                __syncthreads();
+                float f[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = r_lo + 8 * h;
+                    const float mx = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                    f[h] = exp2_fast(m[h] - (mx == -INFINITY ? 0.0f : mx));
+                }
+#pragma unroll
+                for (int w = 0; w < kWN; ++w) {
+                    if (warp == w) {
+#pragma unroll
+                        for (int i = 0; i < kD / 8; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float *d = s_merge + (r_lo + 8 * (e >> 1)) * kD + col(i, e & 1);
+                                const float v = o[i][e] * f[e >> 1];
+                                *d = w == 0 ? v : *d + v;
+                            }
+                    }
+                    __syncthreads();
+                }
+                for (int x = tid; x < rows * (kD / 8); x += 128) {
+                    const int r = x / (kD / 8), c = x % (kD / 8) * 8;
+                    const float mx = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                    const float base = mx == -INFINITY ? 0.0f : mx;
+                    float lt = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWN; ++w) lt += s_l[w][r] * exp2_fast(s_m[w][r] - base);
+                    const float *v = s_merge + r * kD + c;
+                    if (whole) {
+                        const float inv = lt > 0.0f ? p.v_scale / lt : lt == 0.0f ? 0.0f : lt;
+                        const int grow = cur.row0() + r;
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                             (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
+                                              cur.kvh * p.group + grow % p.group) * kD + c;
+                        *reinterpret_cast<uint4 *>(dst) =
+                            make_uint4(bf16x2_of(v[0] * inv, v[1] * inv), bf16x2_of(v[2] * inv, v[3] * inv),
+                                       bf16x2_of(v[4] * inv, v[5] * inv), bf16x2_of(v[6] * inv, v[7] * inv));
+                    } else {
+                        float4 *d = reinterpret_cast<float4 *>(part + r * kD + c);
+                        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        if (c == 0) {
+                            part[kRows * kD + r] = mx;
+                            part[kRows * kD + kRows + r] = lt;
+                        }
+                    }
+                }
+            }
+            if (it + 1 == n_blocks && tid == 0) {
+                AttnDesc d;
+                d.parts = 0;
+                d.qs = cur.r.qs;
+                d.kvh = cur.kvh;
+                d.row0 = cur.row0();
+                d.rows = rows;
+                if (!last && !continued) d.parts = split.parts(blockIdx.x, item_from, cur.nblk);
+                p.desc[blockIdx.x] = d;
+            }
+            if (it + 1 < n_blocks) {
+                cur.next_item(p);
+                fresh_item = true;
+                continued = false;
+                item_from = it + 1;
+                __syncthreads();                 // s_q, s_m and the merge area are read
+            }
+        } else {
+            ++cur.blk;
+        }
+    }
+    cp_async_wait<0>();
+    if (bad && p.status) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+    if (p.wait_at_end) grid_dep_wait();
+}
+
+// Joins the parts of the items that lie in several CTAs' ranges: blockIdx.x is
+// the CTA that started the item, a warp per row, kD / 32 elements a lane.
+template <int kD>
+__global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, int kRows)
+{
+    constexpr int kE = kD / 32;
+    grid_dep_wait();
+    const int c = blockIdx.x;
+    const AttnDesc d = p.desc[c];
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (d.parts < 2 || r >= d.rows) return;
+    const long long stride = static_cast<long long>(kRows) * (kD + 2);
+    // part k of the item
+    auto part = [&](int k) { return p.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
+    float mx = -INFINITY;
+    for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, part(k)[kRows * kD + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float acc[kE], l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+    for (int k = 0; k < d.parts; ++k) {
+        const float *q = part(k);
+        const float f = exp2_fast(q[kRows * kD + r] - base);
+        l += f * q[kRows * kD + kRows + r];
+        float v[kE];
+        if constexpr (kE == 2) {
+            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + r * kD + lane * kE);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kE; e += 4)
+                *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + r * kD + lane * kE + e);
+        }
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] += f * v[e];
+    }
+    const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
+    const int grow = d.row0 + r;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                         (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
+                         lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// CTAs of a kernel that are resident on the GPU at once, found once per kernel
+// and device together with the shared-memory limit.
+template <int kD, bool kE4m3, int kWM>
+static int resident_ctas()
+{
+    using C = AttnCfg<kD, kE4m3, kWM>;
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int n = dev >= 0 && dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        auto kern = paged_attention_kernel<kD, kE4m3, kWM>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return 0;
+        int sms = 0, per = 0;
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, 128, C::kSmem) != cudaSuccess || per < 1) return 0;
+        n = sms * per;
+        if (n > kAttnMaxCtas) n = kAttnMaxCtas;
+        if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int kD, bool kE4m3, int kWM>
+static int launch_mma(AttnParams p, cudaStream_t st, int &launches)
+{
+    using C = AttnCfg<kD, kE4m3, kWM>;
+    const int ctas = resident_ctas<kD, kE4m3, kWM>();
+    if (ctas == 0) return MOE_ERR_CUDA;
+    if (launch_kernel(paged_attention_kernel<kD, kE4m3, kWM>, dim3(ctas), dim3(128), C::kSmem, st, false, p) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (launch_kernel(attention_combine_kernel<kD>, dim3(ctas, (C::kRows + 7) / 8), dim3(256), 0, st, true, p, C::kRows) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    launches += 2;
+    return MOE_OK;
+}
+
+template <int kD>
+static int launch_for_dim(const moe_attn_shape_t &s, const AttnParams &p, cudaStream_t st, int &launches)
+{
+    // up to 16 rows a request one warp-row does, with all four warps along the
+    // keys; beyond, 64-row tiles read the keys a quarter as often
+    const bool few = s.max_q > 0 && static_cast<int64_t>(s.max_q) * p.group <= 16;
+    if (s.cache_dtype == MOE_E4M3)
+        return few ? launch_mma<kD, true, 1>(p, st, launches) : launch_mma<kD, true, 4>(p, st, launches);
+    return few ? launch_mma<kD, false, 1>(p, st, launches) : launch_mma<kD, false, 4>(p, st, launches);
+}
+
+static bool attn_misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+static int check_attn(const moe_attn_shape_t *shape)
+{
+    if (!shape) return MOE_ERR_INVALID_ARG;
+    const moe_attn_shape_t &s = *shape;
+    if (s.B < 1 || s.B > kAttnMaxB || s.num_tokens < 0 || s.n_heads < 1 || s.n_kv_heads < 1 || s.n_heads > 65536 ||
+        s.n_heads % s.n_kv_heads || s.page_size < 1 || s.num_pages < 1 || s.max_pages < 1 ||
+        (s.causal != 0 && s.causal != 1) || s.max_q < 0 || (s.cache_dtype != MOE_BF16 && s.cache_dtype != MOE_E4M3))
+        return MOE_ERR_INVALID_ARG;
+    if (s.head_dim != 64 && s.head_dim != 128 && s.head_dim != 256) return MOE_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(s.num_pages) * s.page_size > 0x7fffffffll || static_cast<int64_t>(s.num_tokens) * s.n_heads > 0x7fffffffll ||
+        static_cast<int64_t>(s.max_pages) * s.page_size > 0x40000000ll)
+        return MOE_ERR_INVALID_ARG;
+    if (s.q_stride && (s.q_stride < static_cast<int64_t>(s.n_heads) * s.head_dim || s.q_stride % 8)) return MOE_ERR_INVALID_ARG;
+    if (s.page_stride && (s.page_stride < static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim || s.page_stride % 16))
+        return MOE_ERR_INVALID_ARG;
+    if (!(s.scale - s.scale == 0.0f)) return MOE_ERR_INVALID_ARG;          // not finite
+    if (s.cache_dtype == MOE_E4M3 && (!(s.k_scale > 0.0f) || !(s.v_scale > 0.0f))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+struct AttnWs {
+    size_t desc, part, total;
+};
+
+static AttnWs attn_ws(const moe_attn_shape_t &s)
+{
+    AttnWs w;
+    w.desc = 0;
+    w.part = (sizeof(AttnDesc) * kAttnMaxCtas + 255) / 256 * 256;
+    const size_t rows = s.max_q > 0 && static_cast<int64_t>(s.max_q) * (s.n_heads / s.n_kv_heads) <= 16 ? 16 : 64;
+    w.total = w.part + static_cast<size_t>(kAttnMaxCtas) * 2 * rows * (s.head_dim + 2) * 4;
+    return w;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes)
+{
+    const int st = check_attn(shape);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = attn_ws(*shape).total;
+    return MOE_OK;
+}
+
+extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_table, const int32_t *q_start, const int32_t *kv_len, void *out,
+                                   int32_t *status, void *ws, size_t ws_bytes, moe_stream_t stream)
+{
+    int &launches = launch_counter();
+    launches = 0;
+    const int st = check_attn(shape);
+    if (st != MOE_OK) return st;
+    const moe_attn_shape_t &s = *shape;
+    if (s.num_tokens == 0) return MOE_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !q_start || !kv_len || !out || !ws) return MOE_ERR_INVALID_ARG;
+    if (attn_misaligned(q) || attn_misaligned(k_cache) || attn_misaligned(v_cache) || attn_misaligned(out) ||
+        (reinterpret_cast<uintptr_t>(ws) & 255))
+        return MOE_ERR_INVALID_ARG;
+    const AttnWs w = attn_ws(s);
+    if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    AttnParams p;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.table = block_table;
+    p.q_start = q_start;
+    p.kv_len = kv_len;
+    p.out = out;
+    p.status = status;
+    p.desc = reinterpret_cast<AttnDesc *>(static_cast<char *>(ws) + w.desc);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + w.part);
+    p.q_stride = s.q_stride ? s.q_stride : static_cast<int64_t>(s.n_heads) * s.head_dim;
+    p.page_stride = s.page_stride ? s.page_stride : static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim;
+    p.B = s.B;
+    p.T = s.num_tokens;
+    p.n_heads = s.n_heads;
+    p.n_kv = s.n_kv_heads;
+    p.group = s.n_heads / s.n_kv_heads;
+    p.page_size = s.page_size;
+    p.num_pages = s.num_pages;
+    p.max_pages = s.max_pages;
+    p.causal = s.causal;
+    p.min_rows = 1;
+    p.max_rows = 0x7fffffff;
+    p.min_blocks = 1;
+    p.wait_at_end = 0;
+    const bool e4m3 = s.cache_dtype == MOE_E4M3;
+    p.scale_log2 = s.scale * (e4m3 ? s.k_scale : 1.0f) * 1.4426950408889634f;
+    p.v_scale = e4m3 ? s.v_scale : 1.0f;
+    cudaStream_t sm = reinterpret_cast<cudaStream_t>(stream);
+    if (s.head_dim == 64) return launch_for_dim<64>(s, p, sm, launches);
+    if (s.head_dim == 128) return launch_for_dim<128>(s, p, sm, launches);
+    return launch_for_dim<256>(s, p, sm, launches);
+}

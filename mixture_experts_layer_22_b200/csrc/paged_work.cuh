@@ -1,0 +1,284 @@
+// paged_work.cuh - how the paged-attention kernels divide a batch among CTAs.
+//
+// An item is one tile of query rows of one request and key/value head: row r of
+// a request is token r / group, query head kv_head * group + r % group, so that
+// the heads that share a key/value head share its loads.  An item has as many
+// blocks of keys as its last row sees.  The blocks of all items, in the order
+// request, key/value head, tile, block, are numbered through, and CTA c of G
+// takes the numbers [W c / G, W (c + 1) / G).  Every CTA thus has the same work
+// however ragged the lengths are, a long sequence is split over many CTAs and
+// neighbours read the same keys at the same time.  An item that lies whole in
+// one CTA's range is written by it; of an item over several CTAs each writes a
+// partial result (unnormalised sums, their maximum and total), and a second
+// kernel joins them in CTA order.  A CTA has at most two partial items: the one
+// it continues (slot 0) and the one it starts and does not finish (slot 1).
+// The division depends on lengths and G alone, so results are reproducible.
+#pragma once
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kAttnMaxB = 4096;
+constexpr int kAttnMaxCtas = 160 * 4;       // resident CTAs of one kernel, at most
+
+// What a combine block needs to know of the item that CTA c started and did not
+// finish: its parts are (c, slot 1), (c + 1, slot 0), ... (c + parts - 1, slot 0).
+struct AttnDesc {
+    int32_t parts;        // 0: none
+    int32_t qs, kvh, row0, rows;
+};
+
+struct AttnParams {
+    const void *q, *k_cache, *v_cache;
+    const int32_t *table, *q_start, *kv_len;
+    void *out;
+    int32_t *status;
+    float *part;          // [G][2][rows * (D + 2)]: sums, then maxima, then totals
+    AttnDesc *desc;       // [G]
+    long long q_stride, page_stride;
+    int B, T, n_heads, n_kv, group, page_size, num_pages, max_pages, causal;
+    int min_rows, max_rows;   // this kernel's requests: rows in [min_rows, max_rows]
+    int min_blocks;           // a CTA gets at least this many blocks
+    int wait_at_end;          // launched while the kernel before it runs
+    float scale_log2, v_scale;
+};
+
+// One request as the kernels see it: n new tokens from row qs on, kv keys.
+// n is 0 for requests that are empty, malformed or another kernel's.
+struct Req {
+    int n, kv, qs;
+};
+
+__device__ __forceinline__ Req attn_request(const AttnParams &p, int b, bool &bad)
+{
+    Req r;
+    const int s = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
+    int kv = __ldg(p.kv_len + b);
+    const long long room = static_cast<long long>(p.max_pages) * p.page_size;
+    if (s < 0 || e < s || e > p.T) {
+        bad = true;
+        r.n = r.kv = r.qs = 0;
+        return r;
+    }
+    if (kv < 0 || kv > room) {
+        bad = true;
+        kv = kv < 0 ? 0 : static_cast<int>(room);
+    }
+    const int rows = (e - s) * p.group;
+    r.n = rows >= p.min_rows && rows <= p.max_rows ? e - s : 0;
+    r.kv = kv;
+    r.qs = s;
+    return r;
+}
+
+// Keys that row `row` of the request sees.
+__device__ __forceinline__ int row_limit(const AttnParams &p, const Req &r, int row)
+{
+    if (!p.causal) return r.kv;
+    const int hi = r.kv - r.n + 1 + row / p.group;
+    return hi < 0 ? 0 : hi;
+}
+
+// Blocks of the tile whose last row is `last`; a row that sees nothing still has
+// its zeros written, so there is at least one.
+template <int kBlk>
+__device__ __forceinline__ int tile_blocks(const AttnParams &p, const Req &r, int last)
+{
+    const int nb = (row_limit(p, r, last) + kBlk - 1) / kBlk;
+    return nb < 1 ? 1 : nb;
+}
+
+// sum over i < m of floor((a i + b) / c), a, b >= 0, c > 0, by the Euclid-like
+// reduction that swaps the roles of a and c.
+__device__ __forceinline__ long long floor_sum(long long m, long long c, long long a, long long b)
+{
+    long long s = 0;
+    for (;;) {
+        if (a >= c) {
+            s += (m - 1) * m / 2 * (a / c);
+            a %= c;
+        }
+        if (b >= c) {
+            s += m * (b / c);
+            b %= c;
+        }
+        const long long y = a * m + b;
+        if (y < c) return s;
+        m = y / c;
+        b = y % c;
+        const long long t = c;
+        c = a;
+        a = t;
+    }
+}
+
+// Blocks of one request and key/value head, all tiles.
+template <int kRows, int kBlk>
+__device__ __forceinline__ long long request_blocks(const AttnParams &p, const Req &r)
+{
+    if (r.n == 0) return 0;
+    const int rows = r.n * p.group, tiles = (rows + kRows - 1) / kRows;
+    if (!p.causal) return static_cast<long long>(tiles) * tile_blocks<kBlk>(p, r, rows - 1);
+    long long s = tile_blocks<kBlk>(p, r, rows - 1);
+    if (kRows % p.group == 0 && r.kv >= r.n) {
+        // the full tiles see kv - n + (i + 1) kRows / group keys
+        const int step = kRows / p.group;
+        if (tiles > 1) s += floor_sum(tiles - 1, kBlk, step, r.kv - r.n + step + kBlk - 1);
+    } else {
+        for (int i = 0; i < tiles - 1; ++i) s += tile_blocks<kBlk>(p, r, (i + 1) * kRows - 1);
+    }
+    return s;
+}
+
+// A position in the numbering, held by every lane of a warp.
+template <int kRows, int kBlk>
+struct Cursor {
+    Req r;
+    int b, kvh, tile, blk, nblk, tiles;
+
+    __device__ __forceinline__ int row0() const { return tile * kRows; }
+    __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kRows, r.n * p.group - tile * kRows); }
+    __device__ __forceinline__ void enter(const AttnParams &p)
+    {
+        nblk = tile_blocks<kBlk>(p, r, min((tile + 1) * kRows, r.n * p.group) - 1);
+    }
+    // On to the next item (warp-collective).  There must be one.
+    __device__ __forceinline__ void next_item(const AttnParams &p)
+    {
+        blk = 0;
+        if (++tile == tiles) {
+            tile = 0;
+            if (++kvh == p.n_kv) {
+                kvh = 0;
+                bool bad = false;
+                const int lane = threadIdx.x & 31;
+                for (int base = b + 1; base < p.B; base += 32) {
+                    const int mine = base + lane;
+                    const bool some = mine < p.B && attn_request(p, mine, bad).n > 0;
+                    const unsigned any = __ballot_sync(0xffffffffu, some);
+                    if (any) {
+                        b = base + __ffs(any) - 1;
+                        break;
+                    }
+                }
+                r = attn_request(p, b, bad);
+                tiles = (r.n * p.group + kRows - 1) / kRows;
+            }
+        }
+        enter(p);
+    }
+};
+
+// The division itself.  init() finds where CTA blockIdx.x starts (cur) and
+// returns how many blocks it has; block-collective over kThreads threads, every
+// thread gets the same answer.
+template <int kThreads, int kRows, int kBlk>
+struct Split {
+    long long W;          // blocks in all
+    int G;                // CTAs that share them
+
+    __device__ __forceinline__ long long cta_start(int c) const { return W * c / G; }
+
+    __device__ __forceinline__ long long init(const AttnParams &p, Cursor<kRows, kBlk> &cur)
+    {
+        __shared__ long long s_warp[kThreads / 32];
+        __shared__ int s_at[4];
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        bool bad = false;
+        long long sum = 0;
+        for (int b = b0; b < b1; ++b) sum += p.n_kv * request_blocks<kRows, kBlk>(p, attn_request(p, b, bad));
+        if (bad && p.status && blockIdx.x == 0) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+        long long inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        long long before = inc - sum;
+        W = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            W += s_warp[w];
+        }
+        const long long most = (W + p.min_blocks - 1) / p.min_blocks;
+        G = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+        const int c = blockIdx.x;
+        if (c >= G) return 0;
+        const long long w0 = cta_start(c), n = cta_start(c + 1) - w0;
+        if (n > 0 && w0 >= before && w0 < before + sum) {
+            // the start lies in this thread's requests
+            long long at = w0 - before;
+            int b = b0;
+            Req r;
+            long long per_head;
+            for (;; ++b) {
+                r = attn_request(p, b, bad);
+                per_head = request_blocks<kRows, kBlk>(p, r);
+                if (at < per_head * p.n_kv) break;
+                at -= per_head * p.n_kv;
+            }
+            const int kvh = static_cast<int>(at / per_head);
+            at -= per_head * kvh;
+            const int rows = r.n * p.group, tiles = (rows + kRows - 1) / kRows;
+            int tile = 0;
+            if (!p.causal) {
+                const int nb = tile_blocks<kBlk>(p, r, rows - 1);
+                tile = static_cast<int>(at / nb);
+                at -= static_cast<long long>(tile) * nb;
+            } else {
+                // the blocks before tile i, by a request cut to its first i
+                // tiles' tokens, or tile by tile
+                if (kRows % p.group == 0 && r.kv >= r.n) {
+                    const int step = kRows / p.group;
+                    const long long base = r.kv - r.n + step + kBlk - 1;
+                    int lo = 0, hi = tiles;           // before(lo) <= at < before(hi)
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (floor_sum(mid, kBlk, step, base) <= at) lo = mid;
+                        else hi = mid;
+                    }
+                    tile = lo;
+                    if (lo > 0) at -= floor_sum(lo, kBlk, step, base);
+                } else {
+                    for (;; ++tile) {
+                        const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * kRows, rows) - 1);
+                        if (at < nb) break;
+                        at -= nb;
+                    }
+                }
+            }
+            s_at[0] = b;
+            s_at[1] = kvh;
+            s_at[2] = tile;
+            s_at[3] = static_cast<int>(at);
+        }
+        __syncthreads();
+        if (n > 0) {
+            cur.b = s_at[0];
+            cur.kvh = s_at[1];
+            cur.tile = s_at[2];
+            cur.blk = s_at[3];
+            cur.r = attn_request(p, cur.b, bad);
+            cur.tiles = (cur.r.n * p.group + kRows - 1) / kRows;
+            cur.enter(p);
+        }
+        return n;
+    }
+
+    // CTAs over which the item extends that CTA c starts at `from_start` blocks
+    // into its range and that has `blocks` blocks.
+    __device__ __forceinline__ int parts(int c, long long from_start, int blocks) const
+    {
+        const long long end = cta_start(c) + from_start + blocks;
+        int k = 1;
+        while (cta_start(c + k) < end) ++k;
+        return k;
+    }
+};
+
+}  // namespace moe

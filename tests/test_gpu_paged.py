@@ -1,0 +1,506 @@
+"""GPU tests of the paged-attention operators against 64-bit forms of their
+definitions."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_22_b200 as moe
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+CHECK = -5       # MOE_ERR_DEVICE_CHECK
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ the plan
+def _plan(cached, fresh, free, table, ps, num_pages, max_tokens, free_pos=None, status=None):
+    B, max_pages = table.shape
+    s = moe.PageShape(B=B, max_tokens=max_tokens, max_pages=max_pages, page_size=ps, num_pages=num_pages, n_free=len(free))
+    t = _i32(table)
+    q_start, kv_len = _i32([-7] * (B + 1)), _i32([-7] * B)
+    pos, slot = _i32([-7] * max_tokens), _i32([-7] * max_tokens)
+    nxt = _i32([-7])
+    moe.page_plan(s, _i32(cached), _i32(fresh), _i32(free), t, q_start, kv_len, pos, slot, nxt,
+                  None if free_pos is None else _i32([free_pos]), status)
+    torch.cuda.synchronize()
+    return [x.cpu().numpy() for x in (t, q_start, kv_len, pos, slot)] + [int(nxt[0])]
+
+
+def _check_plan(cached, fresh, ps, *, spare=5, pad=0, free_pos=0, short=0, seed=0):
+    r = np.random.default_rng(seed)
+    B = len(cached)
+    held = [-(-c // ps) for c in cached]
+    need = [-(-(c + f) // ps) for c, f in zip(cached, fresh)]
+    num_pages = sum(need) + spare
+    order = r.permutation(num_pages).astype(np.int32)
+    table = np.full((B, max(max(need), 1) + 1), -1, np.int32)
+    at = 0
+    for b, n in enumerate(held):
+        table[b, :n] = order[at:at + n]
+        at += n
+    free = np.concatenate([np.full(free_pos, 3, np.int32), order[at:]])
+    free = free[:len(free) - spare - short] if short else free
+    rows = sum(fresh) + pad
+    status = _i32([0])
+    got = _plan(cached, fresh, free, table, ps, num_pages, rows, free_pos, status)
+    *want, bad = ref.plan(cached, fresh, free, free_pos, table, ps, num_pages, rows)
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w)
+    assert int(status[0]) == (CHECK if bad else 0) and bad == (short > 0)
+
+
+@pytest.mark.parametrize("cached,fresh,ps,kw", [
+    ([0], [1], 16, {}), ([15], [1], 16, {}), ([16], [1], 16, {}), ([16], [0], 16, {}), ([0], [0], 16, {}),
+    ([5, 0, 31], [0, 3, 40], 16, dict(pad=7)), ([7, 7, 7], [1, 1, 1], 1, {}), ([3, 100], [97, 28], 128, dict(free_pos=2)),
+    ([10, 10, 10, 10], [5, 60, 5, 5], 10, dict(short=2)), ([0, 0], [33, 1], 16, dict(short=4))])
+def test_plan_small(cached, fresh, ps, kw):
+    _check_plan(cached, fresh, ps, **kw)
+
+
+@pytest.mark.parametrize("B,seed", [(31, 1), (512, 2), (513, 3), (1025, 4), (4096, 5)])
+def test_plan_random(B, seed):
+    r = np.random.default_rng(seed)
+    fresh = r.integers(0, 5, B)
+    fresh[r.integers(B)] = 700
+    fresh[:40] = 0                                       # a run of requests without tokens
+    _check_plan(r.integers(0, 300, B).tolist(), fresh.tolist(), int(r.integers(1, 40)), pad=int(r.integers(0, 900)), seed=seed)
+
+
+def test_plan_refuses_bad_requests_and_pages():
+    """Negative and over-long lengths, page ids outside the cache, a cursor
+    outside the list, more tokens than rows: flagged, and nothing out of place."""
+    for cached, fresh, free, pos, table, rows in [
+            ([-1, 4], [2, 3], [5, 6, 7], 0, [[1, 2], [3, -1]], 9), ([4, 4], [-2, 3], [5, 6, 7], 0, [[1, 2], [3, -1]], 9),
+            ([4, 4], [5, 3], [5, 6, 7], 0, [[1, 2], [3, -1]], 9), ([4, 4], [2, 3], [5, 99, 7], 0, [[1, -1], [3, -1]], 9),
+            ([3, 3], [3, 3], [5, 6, 7], 0, [[99, -1], [-4, -1]], 9), ([3, 3], [3, 3], [5, 6, 7], 4, [[1, -1], [2, -1]], 9),
+            ([3, 3], [3, 3], [5, 6, 7], -1, [[1, -1], [2, -1]], 9), ([3, 3], [3, 3], [5, 6, 7], 1, [[1, -1], [2, -1]], 4),
+            ([2 ** 31 - 1, 3], [2 ** 31 - 1, 3], [5, 6, 7], 1, [[1, -1], [2, -1]], 4)]:
+        table = np.array(table, np.int32)
+        status = _i32([0])
+        got = _plan(cached, fresh, free, table, 4, 10, rows, pos, status)
+        *want, bad = ref.plan(cached, fresh, free, pos, table, 4, 10, rows)
+        assert bad and int(status[0]) == CHECK
+        for g, w in zip(got, want):
+            assert np.array_equal(g, w)
+
+
+# ---------------------------------------------------------------- the append
+def _append_case(T, heads, kv_heads, dim, rot, *, il=False, e4m3=False, ps=16, pad=0, qkv=True, inplace=False, alternate=False,
+                 seed=0, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    rows, num_pages, max_pos = T + pad, -(-T // ps) + 3, 500
+    if qkv:
+        x = (torch.randn(rows, heads + 2 * kv_heads, dim, generator=g) * spread).to(torch.bfloat16)
+        q, k, v = x[:, :heads], x[:, heads:heads + kv_heads], x[:, heads + kv_heads:]
+        dx = x.cuda()
+        dq, dk, dv = dx[:, :heads], dx[:, heads:heads + kv_heads], dx[:, heads + kv_heads:]
+        st = x.stride(0)
+    else:
+        q, k, v = ((torch.randn(rows, h, dim, generator=g) * spread).to(torch.bfloat16) for h in (heads, kv_heads, kv_heads))
+        dq, dk, dv = q.cuda(), k.cuda(), v.cuda()
+        st = 0
+    pos = torch.randint(0, max_pos, (rows,), generator=g, dtype=torch.int32)
+    slots = torch.full((rows,), -1, dtype=torch.int32)
+    where = torch.randperm(rows, generator=g)[:T]            # padding rows anywhere
+    slots[where] = torch.randperm(num_pages * ps, generator=g)[:T].to(torch.int32)
+    ang = torch.rand(max_pos, max(rot // 2, 1), generator=g, dtype=torch.float64) * 6.3
+    cos_sin = torch.cat([ang.cos(), ang.sin()], 1)[:, :max(rot, 1)].float() if rot else None
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    shape = (num_pages, ps, kv_heads, dim)
+    if alternate:
+        both = torch.zeros((num_pages, 2) + shape[1:], dtype=dt, device="cuda")
+        kc, vc = both[:, 0], both[:, 1]
+    else:
+        kc, vc = torch.zeros(shape, dtype=dt, device="cuda"), torch.zeros(shape, dtype=dt, device="cuda")
+    q_out = dq if inplace else torch.full((rows, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    ks, vs = (1 / 64, 0.017) if e4m3 else (1.0, 1.0)
+    s = moe.AppendShape(num_tokens=rows, n_heads=heads, n_kv_heads=kv_heads, head_dim=dim, rot_dim=rot, max_pos=max_pos,
+                        interleaved=int(il), page_size=ps, num_pages=num_pages, cache_dtype=int(e4m3), q_stride=st, k_stride=st,
+                        v_stride=st, page_stride=kc.stride(0) if alternate else 0, k_scale=ks, v_scale=vs)
+    status = _i32([0])
+    moe.rope_append(s, dq, dk, dv, pos.cuda() if rot else None, slots.cuda(), cos_sin.cuda() if rot else None, q_out, kc, vc, status)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    valid = slots >= 0
+    rq, rk, rv = ref.rotate(q.double(), cos_sin, pos, rot, il), ref.rotate(k.double(), cos_sin, pos, rot, il), v.double()
+
+    def near(got, want, size, u, step):
+        # the store's rounding; two products and a sum of terms up to `size`, each rounded in
+        # fp32; `step`: half the spacing of the type's subnormals
+        assert ((got - want).abs() <= u * want.abs() + 3 * ref.U_F32 * (1 + u) * size + step).all()
+
+    qsize, ksize = (x.double().abs().amax(-1, keepdim=True) * 2 for x in (q, k))
+    got = q_out.cpu().double()
+    near(got[valid], rq[valid], qsize[valid], ref.U_BF16, 0.0)
+    # a row without a slot keeps what it held
+    assert (got[~valid] == (q.double()[~valid] if inplace else 7.0)).all()
+    for cache, want, size, sc in ((kc, rk, ksize, ks), (vc, rv, rv.abs(), vs)):
+        got = ref.cache_values(cache.cpu().contiguous()).flatten(0, 1)
+        at = slots[valid].long()
+        if e4m3:
+            w = (want[valid] / sc).clamp(-448, 448)
+            near(got[at], w, size[valid] / sc, ref.U_E4M3, 2.0 ** -10)
+        else:
+            near(got[at], want[valid], size[valid], ref.U_BF16, 0.0)
+        rest = torch.ones(got.shape[0], dtype=torch.bool)
+        rest[at] = False
+        assert (got[rest] == 0).all()
+
+
+@pytest.mark.parametrize("T,heads,kv_heads,dim,rot,kw", [
+    (1, 1, 1, 64, 64, {}), (1, 32, 8, 128, 128, {}), (7, 8, 2, 128, 128, dict(pad=3)), (33, 5, 5, 64, 32, dict(il=True)),
+    (33, 5, 5, 64, 48, dict(qkv=False)), (20, 3, 1, 256, 256, {}), (20, 3, 1, 256, 96, dict(il=True, e4m3=True)),
+    (50, 8, 2, 128, 128, dict(e4m3=True, pad=9)), (50, 8, 2, 64, 22, dict(il=True, e4m3=True)), (17, 4, 4, 128, 0, {}),
+    (17, 4, 4, 128, 0, dict(e4m3=True)), (40, 4, 2, 128, 64, dict(qkv=False, inplace=True, pad=5)),
+    (40, 4, 2, 128, 128, dict(alternate=True)), (40, 4, 2, 64, 64, dict(alternate=True, e4m3=True, ps=5)),
+    (64, 77, 3, 64, 64, dict(ps=1)), (64, 8, 2, 128, 128, dict(e4m3=True, spread=20.0)), (6000, 3, 1, 64, 64, {}),
+    (1500, 128, 8, 64, 64, dict(il=True, e4m3=True)), (2500, 32, 8, 128, 128, dict(pad=100))])
+def test_append(T, heads, kv_heads, dim, rot, kw):
+    _append_case(T, heads, kv_heads, dim, rot, **kw)
+
+
+def test_append_is_undone_by_the_inverse_step():
+    """The inverse step on the rotated queries gives the queries back, to two
+    bf16 roundings and the code's."""
+    T, H, D = 50, 4, 128
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(T, H, D, generator=g).to(torch.bfloat16)
+    pos = torch.randint(0, 100, (T,), generator=g, dtype=torch.int32).cuda()
+    w = 1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)
+    ang = torch.arange(100, dtype=torch.float64)[:, None] * w
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    out = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros(4, 16, 1, D, dtype=torch.bfloat16, device="cuda")
+    s = moe.AppendShape(num_tokens=T, n_heads=H, n_kv_heads=1, head_dim=D, rot_dim=D, max_pos=100, page_size=16, num_pages=4)
+    kv = torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    moe.rope_append(s, q.cuda(), kv, kv, pos, torch.arange(T, dtype=torch.int32, device="cuda"), cs, out, cache, cache)
+    codes = torch.empty(T, H, D, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(T, H, dtype=torch.float32, device="cuda")
+    moe.inv_rope_quant(moe.RopeShape(num_tokens=T, n_heads=H, head_dim=D, rot_dim=D, max_pos=100), out, pos, cs, codes, scales)
+    back = codes.view(torch.float8_e4m3fn).double().cpu() * scales.double().cpu()[..., None]
+    q = q.double()
+    size = q.abs().amax(-1, keepdim=True)
+    # a pair's rounding of 2^-8 each turns into at most sqrt(2) 2^-8 of its larger member; the code adds 2^-4 of the value
+    # and half its smallest step, 2^-10 of size / 448
+    assert ((back - q).abs() <= ref.U_E4M3 * q.abs() + size * (1.5 * 2 ** -8 * (1 + ref.U_E4M3) + 2 ** -10 / 448 * 1.1)).all()
+
+
+def test_append_flags_bad_slots_and_positions():
+    T, D = 6, 64
+    x = torch.randn(T, 3, D).to(torch.bfloat16).cuda()
+    cs = torch.zeros(10, D, device="cuda")
+    for slots, pos in [([0, 1, -2, 3, 4, 5], [0] * 6), ([0, 1, 64, 3, 4, 5], [0] * 6), ([0, 1, 2, 3, 4, 5], [0, 0, 10, 0, 0, 0]),
+                       ([0, 1, 2, 3, 4, 5], [0, 0, -1, 0, 0, 0])]:
+        kc, vc = torch.full((4, 16, 1, D), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 16, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = torch.full((T, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        status = _i32([0])
+        s = moe.AppendShape(num_tokens=T, n_heads=1, n_kv_heads=1, head_dim=D, rot_dim=D, max_pos=10, page_size=16, num_pages=4,
+                            q_stride=3 * D, k_stride=3 * D, v_stride=3 * D)
+        moe.rope_append(s, x[:, :1], x[:, 1:2], x[:, 2:], _i32(pos), _i32(slots), cs, out, kc, vc, status)
+        assert int(status[0]) == CHECK
+        assert (out[2] == 7).all() and (out[[0, 1, 3, 4, 5]] == 0).all()
+        assert (vc.flatten(0, 1)[[0, 1, 3, 4, 5], 0] == x[[0, 1, 3, 4, 5], 2]).all()
+        keep = torch.ones(64, dtype=torch.bool)
+        keep[[0, 1, 3, 4, 5]] = False
+        assert (vc.flatten(0, 1)[keep] == 7).all()
+
+
+# -------------------------------------------------------------- the attention
+class Dev:
+    """A batch on the device."""
+
+    def __init__(self, b: ref.Batch, max_q=None, out_fill=7.0):
+        self.b = b
+        if b.page_stride:
+            both = torch.stack([b.k_cache, b.v_cache], 1).cuda()
+            self.k_cache, self.v_cache = both[:, 0], both[:, 1]
+        else:
+            self.k_cache, self.v_cache = b.k_cache.cuda(), b.v_cache.cuda()
+        if b.q_stride:
+            self.q = torch.zeros(b.T, b.q_stride, dtype=torch.bfloat16, device="cuda").as_strided(
+                (b.T, b.heads, b.dim), (b.q_stride, b.dim, 1))
+            self.q.copy_(b.q)
+        else:
+            self.q = b.q.cuda()
+        self.table, self.q_start, self.kv_len = b.table.cuda(), b.q_start.cuda(), b.kv_len.cuda()
+        self.out = torch.full((b.T, b.heads, b.dim), out_fill, dtype=torch.bfloat16, device="cuda")
+        self.shape = moe.AttnShape(
+            B=b.B, num_tokens=b.T, n_heads=b.heads, n_kv_heads=b.kv_heads, head_dim=b.dim, page_size=b.ps,
+            num_pages=b.num_pages, max_pages=b.max_pages, causal=int(b.causal), max_q=max(b.q_lens) if max_q is None else max_q,
+            cache_dtype=int(b.e4m3), q_stride=b.q_stride, page_stride=b.page_stride, scale=b.scale, k_scale=b.kv_scale,
+            v_scale=b.kv_scale)
+        self.ws = moe.attn_workspace(self.shape)
+        self.ws.fill_(0xFF)                              # its contents do not matter
+        self.status = _i32([0])
+
+    def run(self):
+        moe.paged_attention(self.shape, self.q, self.k_cache, self.v_cache, self.table, self.q_start, self.kv_len, self.out,
+                            self.ws, self.status)
+        return self.out
+
+
+def _check_attn(b, max_q=None):
+    d = Dev(b, max_q)
+    out = d.run().cpu().double()
+    assert int(d.status[0]) == 0
+    n = sum(b.q_lens)
+    want, tol = b.reference()
+    err = (out[:n] - want).abs()
+    assert torch.isfinite(out[:n]).all()
+    assert (err <= tol).all(), f"{float((err / tol).max()):.2f} of the bound"
+    assert (out[n:] == 7).all()                          # rows behind the last request
+    return d
+
+
+LENGTHS = {
+    "one key": ([1], [1]),
+    "decode": ([1, 1, 1, 1], [1, 17, 64, 300]),
+    "long and short": ([1] * 6, [2000, 1, 65, 700, 3, 129]),
+    "chunks": ([5, 1, 40, 0, 16], [5, 100, 77, 30, 16]),
+    "prompt": ([200], [200]),
+    "chunk behind a prefix": ([130], [400]),
+    "nothing cached": ([1, 0, 2], [0, 0, 33]),
+    "more new than keys": ([6, 3], [4, 3]),
+    "spans": ([2, 3, 4, 1], [128, 64, 256, 192]),
+    "big": ([300, 1, 70], [900, 1500, 1000]),
+}
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("name", list(LENGTHS))
+def test_attention_lengths(name, dim, e4m3):
+    q, kv = LENGTHS[name]
+    _check_attn(ref.Batch(q, kv, heads=4, kv_heads=2, dim=dim, e4m3=e4m3, pad_rows=2))
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 8), (8, 1), (28, 4), (12, 4), (16, 1), (24, 1), (10, 2)])
+@pytest.mark.parametrize("q,kv", [([1, 1, 1], [200, 31, 513]), ([9, 50, 1], [9, 170, 300])], ids=["decode", "chunks"])
+def test_attention_head_layouts(heads, kv_heads, q, kv):
+    _check_attn(ref.Batch(q, kv, heads=heads, kv_heads=kv_heads, dim=64, seed=1))
+    _check_attn(ref.Batch(q, kv, heads=heads, kv_heads=kv_heads, dim=128, e4m3=True, seed=2))
+
+
+@pytest.mark.parametrize("ps", [1, 3, 8, 16, 24, 32, 64, 100, 128, 256, 512])
+def test_attention_page_sizes(ps):
+    _check_attn(ref.Batch([1, 60, 1], [130, 300, 600], heads=4, kv_heads=2, dim=128, ps=ps, seed=3))
+    _check_attn(ref.Batch([1, 60, 1], [130, 300, 600], heads=4, kv_heads=2, dim=64, ps=ps, e4m3=True, seed=3))
+
+
+@pytest.mark.parametrize("kw", [dict(causal=False), dict(interleaved_kv=True), dict(qkv=True),
+                                dict(qkv=True, interleaved_kv=True, e4m3=True), dict(spread=30.0), dict(spread=30.0, e4m3=True),
+                                dict(spread=0.0), dict(spread=1e-30, e4m3=True)],
+                         ids=lambda kw: ",".join(map(str, kw.items())))
+@pytest.mark.parametrize("max_q", [None, 0, 1, 1000])
+def test_attention_forms_and_hints(kw, max_q):
+    """Strides, no mask, flat and peaked scores; any hint about the longest request."""
+    _check_attn(ref.Batch([1, 45, 2, 1], [130, 300, 2, 700], heads=8, kv_heads=2, dim=128, seed=4, **kw), max_q)
+
+
+def test_attention_flags_bad_data_and_stays_in_bounds():
+    b = ref.Batch([2, 3, 1], [40, 50, 60], heads=4, kv_heads=2, dim=64, seed=5)
+    want, tol = b.reference()
+    rows = {0: slice(0, 2), 1: slice(2, 5), 2: slice(5, 6)}
+
+    def run(change, ok):
+        for max_q in (3, 1000):
+            d = Dev(b, max_q)
+            change(d)
+            out = d.run().cpu().double()
+            assert int(d.status[0]) == CHECK
+            for i in ok:
+                assert ((out[rows[i]] - want[rows[i]]).abs() <= tol[rows[i]]).all()
+        return out
+
+    def page(x):
+        def f(d):
+            d.table[1, 2] = x
+        return f
+    for x in (-1, b.num_pages, 2 ** 31 - 1, -2 ** 31):
+        out = run(page(x), [0, 2])
+        # that page's keys count as zeros
+        z = ref.Batch([2, 3, 1], [40, 50, 60], heads=4, kv_heads=2, dim=64, seed=5)
+        z.k[1][32:48] = 0
+        z.v[1][32:48] = 0
+        w2, t2 = z.reference()
+        assert ((out[rows[1]] - w2[rows[1]]).abs() <= t2[rows[1]]).all()
+
+    def kv(x):
+        def f(d):
+            d.kv_len[0] = x
+        return f
+    assert (run(kv(-3), [1, 2])[rows[0]] == 0).all()
+    run(kv(2 ** 31 - 1), [1, 2])
+
+    def start(i, x):
+        def f(d):
+            d.q_start[i] = x
+        return f
+    assert (run(start(3, 100), [0, 1])[rows[2]] == 7).all()
+    assert (run(start(0, -1), [1, 2])[rows[0]] == 7).all()
+    assert (run(start(1, 9), [2])[rows[0]] == 7).all()
+
+
+def test_attention_same_bits_every_time_on_streams_and_in_graphs():
+    b = ref.Batch([1, 70, 1, 3], [900, 300, 40, 1200], heads=8, kv_heads=2, dim=128, seed=6)
+    d = Dev(b)
+    first = d.run().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    d.out.fill_(7)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        d.run()
+    side.synchronize()
+    assert torch.equal(first, d.out)
+    e = Dev(ref.Batch([1, 1], [800, 90], heads=8, kv_heads=2, dim=128, seed=7), 70)
+    e.ws = d.ws                                          # two graphs, one workspace, replayed in turn
+    other = e.run().clone()
+    graphs = []
+    for x in (d, e):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.run()
+        graphs.append(g)
+    for _ in range(3):
+        d.out.fill_(7)
+        e.out.fill_(7)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, d.out) and torch.equal(other, e.out)
+    # a captured call follows its lengths: the same graph, other tables
+    short = ref.Batch([1, 70, 1, 3], [100, 70, 40, 3], heads=8, kv_heads=2, dim=128, seed=8)
+    for name in ("k_cache", "v_cache"):
+        getattr(d, name)[:short.num_pages].copy_(getattr(short, name))
+    d.q.copy_(short.q)
+    d.table[:, :short.max_pages].copy_(short.table)
+    d.kv_len.copy_(short.kv_len)
+    graphs[0].replay()
+    want, tol = short.reference()
+    assert ((d.out.cpu().double() - want).abs() <= tol).all()
+
+
+def test_attention_offsets_beyond_32_bits():
+    """Pages whose elements lie more than 2^31 (and bytes more than 2^32) into the
+    cache."""
+    ps, g, dim = 64, 8, 128
+    pages = 2 ** 31 // (ps * g * dim) + 40
+    k_cache = torch.zeros(pages, ps, g, dim, dtype=torch.bfloat16, device="cuda")
+    b = ref.Batch([1, 40], [100, 130], heads=16, kv_heads=g, dim=dim, ps=ps, seed=9)
+    d = Dev(b)
+    shift = pages - b.num_pages
+    k_cache[shift:].copy_(d.k_cache)
+    k_cache[:shift].fill_(float("nan"))
+    v_cache = k_cache.clone()
+    v_cache[shift:].copy_(d.v_cache)
+    d.k_cache, d.v_cache = k_cache, v_cache
+    d.table = torch.where(d.table >= 0, d.table + shift, d.table)
+    d.shape.num_pages = pages
+    out = d.run().cpu().double()
+    want, tol = b.reference()
+    assert int(d.status[0]) == 0 and ((out - want).abs() <= tol).all()
+
+
+def test_binding_refuses_wrong_tensors():
+    d = Dev(ref.Batch([1], [20], heads=4, kv_heads=2, dim=64))
+    args = dict(q=d.q, k_cache=d.k_cache, v_cache=d.v_cache, block_table=d.table, q_start=d.q_start, kv_len=d.kv_len, out=d.out,
+                ws=d.ws)
+    for name, bad in [("q", d.q.float()), ("q", d.q[:, :2]), ("k_cache", d.k_cache.transpose(1, 2)),
+                      ("v_cache", d.v_cache.view(torch.int16)), ("block_table", d.table.long()), ("kv_len", d.kv_len.cpu()),
+                      ("q_start", d.q_start[:1]), ("out", d.out.transpose(0, 1))]:
+        with pytest.raises(ValueError):
+            moe.paged_attention(d.shape, **{**args, name: bad})
+
+
+# ------------------------------------------------- one attention step of a layer
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_steps_of_a_served_batch(e4m3):
+    """Prompts, then single tokens, through plan, append, attention and the
+    inverse rotary step, in a graph replayed step by step, against 64-bit
+    attention over the stored cache."""
+    B, H, G, D, ps, steps = 5, 8, 2, 128, 16, 4
+    g = torch.Generator().manual_seed(11)
+    prompts = [33, 1, 16, 100, 7]
+    num_pages, max_pages, max_pos = 40, 9, 256
+    w = 1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * w
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    sc = 1 / 64 if e4m3 else 1.0
+    kc = torch.full((num_pages, ps, G, D), 0x7F if e4m3 else float("nan"), dtype=dt, device="cuda")
+    vc = kc.clone()
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(num_pages, generator=g).to(torch.int32).cuda()
+    cached, fresh, pos_now, pos_next = (_i32(x) for x in ([0] * B, prompts, [0], [0]))
+    csd, status = cs.cuda(), _i32([0])
+
+    def buffers(rows):
+        return dict(x=torch.zeros(rows, H + 2 * G, D, dtype=torch.bfloat16, device="cuda"), q_start=_i32([0] * (B + 1)),
+                    kv_len=_i32([0] * B), positions=_i32([0] * rows), slots=_i32([0] * rows),
+                    q=torch.zeros(rows, H, D, dtype=torch.bfloat16, device="cuda"),
+                    out=torch.full((rows, H, D), 7.0, dtype=torch.bfloat16, device="cuda"),
+                    codes=torch.zeros(rows, H, D, dtype=torch.uint8, device="cuda"), scales=torch.zeros(rows, H, device="cuda"))
+
+    def step(f, rows, max_q):
+        moe.page_plan(moe.PageShape(B=B, max_tokens=rows, max_pages=max_pages, page_size=ps, num_pages=num_pages, n_free=num_pages),
+                      cached, fresh, free, table, f["q_start"], f["kv_len"], f["positions"], f["slots"], pos_next, pos_now, status)
+        st = (H + 2 * G) * D
+        moe.rope_append(moe.AppendShape(num_tokens=rows, n_heads=H, n_kv_heads=G, head_dim=D, rot_dim=D, max_pos=max_pos, page_size=ps,
+                                        num_pages=num_pages, cache_dtype=int(e4m3), q_stride=st, k_stride=st, v_stride=st, k_scale=sc,
+                                        v_scale=sc),
+                        f["x"][:, :H], f["x"][:, H:H + G], f["x"][:, H + G:], f["positions"], f["slots"], csd, f["q"], kc, vc, status)
+        s = moe.AttnShape(B=B, num_tokens=rows, n_heads=H, n_kv_heads=G, head_dim=D, page_size=ps, num_pages=num_pages,
+                          max_pages=max_pages, causal=1, max_q=max_q, cache_dtype=int(e4m3), scale=D ** -0.5, k_scale=sc, v_scale=sc)
+        f["ws"] = f.get("ws", None) if f.get("ws") is not None else moe.attn_workspace(s)
+        moe.paged_attention(s, f["q"], kc, vc, table, f["q_start"], f["kv_len"], f["out"], f["ws"], status)
+        moe.inv_rope_quant(moe.RopeShape(num_tokens=rows, n_heads=H, head_dim=D, rot_dim=D, max_pos=max_pos), f["out"], f["positions"],
+                           csd, f["codes"], f["scales"], status)
+        cached.copy_(f["kv_len"])
+        pos_now.copy_(pos_next)
+
+    def check(f, lens, n):
+        torch.cuda.synchronize()
+        assert int(status[0]) == 0
+        t, q = table.cpu(), f["q"][:n].cpu().double()
+        k, v = [], []
+        kv_lens = f["kv_len"].tolist()
+        for b, kv in enumerate(kv_lens):
+            ids = t[b, :-(-kv // ps)].long()
+            for c, rows in ((kc, k), (vc, v)):
+                rows.append(ref.cache_values(c.cpu()[ids]).flatten(0, 1)[:kv] * sc)
+                assert torch.isfinite(rows[-1]).all()
+        out = f["out"].cpu().double()
+        want, tol = ref.attention(q, k, v, lens, kv_lens, True, D ** -0.5, ref.U_F16 if e4m3 else ref.U_BF16)
+        assert ((out[:n] - want).abs() <= tol).all()
+        back = ref.rotate(out[:n], torch.cat([cs[:, :D // 2], -cs[:, D // 2:]], 1), f["positions"][:n].cpu(), D, False)
+        got = f["codes"].view(torch.float8_e4m3fn).cpu().double()[:n] * f["scales"].cpu().double()[:n, :, None]
+        size = back.abs().amax(-1, keepdim=True)
+        assert ((got - back).abs() <= ref.U_E4M3 * back.abs() + size * (2 ** -10 / 448 * 1.1 + 2 ** -20)).all()
+
+    n = sum(prompts)
+    f = buffers(n + 3)
+    f["x"][:n] = torch.randn(n, H + 2 * G, D, generator=g).to(torch.bfloat16).cuda()
+    step(f, n + 3, max(prompts))
+    check(f, prompts, n)
+    assert (f["out"][n:] == 7).all()
+    f = buffers(B)
+    fresh.fill_(1)
+    cached_was, pos_was, table_was = cached.clone(), pos_now.clone(), table.clone()
+    graph = torch.cuda.CUDAGraph()
+    step(f, B, 1)                                        # once outside, as a capture's warm-up
+    cached.copy_(cached_was)
+    pos_now.copy_(pos_was)
+    table.copy_(table_was)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(f, B, 1)
+    for i in range(steps):
+        f["x"].copy_(torch.randn(B, H + 2 * G, D, generator=g).to(torch.bfloat16))
+        graph.replay()
+        check(f, [1] * B, B)
+    assert f["kv_len"].tolist() == [n + steps for n in prompts]
