@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
     if (n_blocks == 0) {
         if (tid == 0) p.desc[blockIdx.x].parts = 0;
         grid_dep_launch();
+        if (p.wait_at_end) grid_dep_wait();
         return;
     }
     grid_dep_launch();
@@ -560,20 +561,32 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
     if (p.wait_at_end) grid_dep_wait();
 }
 
-// Joins the parts of the items that lie in several CTAs' ranges: blockIdx.x is
-// the CTA that started the item, a warp per row, kD / 32 elements a lane.
+// The partial results of one kernel.
+struct AttnParts {
+    const float *part;
+    const AttnDesc *desc;
+    int ctas, rows;
+};
+
+// Joins the parts of the items that lie in several CTAs' ranges, of one or two
+// kernels: blockIdx.x is the CTA that started the item, a warp per row, kD / 32
+// elements a lane.
 template <int kD>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, int kRows)
+__global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, const AttnParts few, const AttnParts many)
 {
     constexpr int kE = kD / 32;
-    grid_dep_wait();
-    const int c = blockIdx.x;
-    const AttnDesc d = p.desc[c];
+    const bool second = static_cast<int>(blockIdx.x) >= few.ctas;
+    const int c = second ? blockIdx.x - few.ctas : blockIdx.x;
+    const int kRows = second ? many.rows : few.rows;
+    const float *parts = second ? many.part : few.part;
     const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (r >= kRows) return;
+    grid_dep_wait();
+    const AttnDesc d = second ? many.desc[c] : few.desc[c];
     if (d.parts < 2 || r >= d.rows) return;
     const long long stride = static_cast<long long>(kRows) * (kD + 2);
     // part k of the item
-    auto part = [&](int k) { return p.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
+    auto part = [&](int k) { return parts + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
     float mx = -INFINITY;
     for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, part(k)[kRows * kD + r]);
 #pragma unroll
@@ -630,29 +643,82 @@ static int resident_ctas()
 }
 
 template <int kD, bool kE4m3, int kWM>
-static int launch_mma(AttnParams p, cudaStream_t st, int &launches)
+static int launch_mma(const AttnParams &p, AttnParts &parts, bool chained, cudaStream_t st)
 {
     using C = AttnCfg<kD, kE4m3, kWM>;
-    const int ctas = resident_ctas<kD, kE4m3, kWM>();
-    if (ctas == 0) return MOE_ERR_CUDA;
-    if (launch_kernel(paged_attention_kernel<kD, kE4m3, kWM>, dim3(ctas), dim3(128), C::kSmem, st, false, p) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    if (launch_kernel(attention_combine_kernel<kD>, dim3(ctas, (C::kRows + 7) / 8), dim3(256), 0, st, true, p, C::kRows) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
-    launches += 2;
-    return MOE_OK;
+    parts = AttnParts{p.part, p.desc, resident_ctas<kD, kE4m3, kWM>(), C::kRows};
+    if (parts.ctas == 0) return MOE_ERR_CUDA;
+    return launch_kernel(paged_attention_kernel<kD, kE4m3, kWM>, dim3(parts.ctas), dim3(128), C::kSmem, st, chained, p) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+// Requests of up to 16 rows go to the kernel whose tile is 16 rows, the others to
+// the tensor-memory kernel, or where that does not take the shape, to 64-row
+// tiles.  A batch that by its hint has only the former is one kernel's.  The
+// second kernel starts while the first one ends.
+constexpr int kFewRows = 16;
+
+static bool only_few(const moe_attn_shape_t &s)
+{
+    return s.max_q > 0 && static_cast<int64_t>(s.max_q) * (s.n_heads / s.n_kv_heads) <= kFewRows;
+}
+
+// Workspace: descriptors and partial results of either kernel.
+struct AttnWs {
+    size_t few_desc, many_desc, few_part, many_part, total;
+};
+
+static AttnWs attn_ws(const moe_attn_shape_t &s)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    auto parts = [&](int ctas, int rows) { return up(static_cast<size_t>(ctas) * 2 * rows * (s.head_dim + 2) * 4); };
+    AttnWs w;
+    w.few_desc = 0;
+    w.many_desc = up(sizeof(AttnDesc) * kAttnMaxCtas);
+    w.few_part = 2 * w.many_desc;
+    w.many_part = w.few_part + parts(kAttnMaxCtas, kFewRows);
+    w.total = w.many_part;
+    if (!only_few(s)) w.total += attn_tc_takes(s) ? parts(kAttnTcMaxCtas, 256) : parts(kAttnMaxCtas, 64);
+    return w;
 }
 
 template <int kD>
-static int launch_for_dim(const moe_attn_shape_t &s, const AttnParams &p, cudaStream_t st, int &launches)
+static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, cudaStream_t st, int &launches)
 {
-    // up to 16 rows a request one warp-row does, with all four warps along the
-    // keys; beyond, 64-row tiles read the keys a quarter as often
-    const bool few = s.max_q > 0 && static_cast<int64_t>(s.max_q) * p.group <= 16;
-    if (s.cache_dtype == MOE_E4M3)
-        return few ? launch_mma<kD, true, 1>(p, st, launches) : launch_mma<kD, true, 4>(p, st, launches);
-    return few ? launch_mma<kD, false, 1>(p, st, launches) : launch_mma<kD, false, 4>(p, st, launches);
+    const AttnWs w = attn_ws(s);
+    const bool e4m3 = s.cache_dtype == MOE_E4M3;
+    AttnParts few, many = {nullptr, nullptr, 0, 0};
+    p.desc = reinterpret_cast<AttnDesc *>(ws + w.few_desc);
+    p.part = reinterpret_cast<float *>(ws + w.few_part);
+    p.min_rows = 1;
+    p.max_rows = only_few(s) ? 0x7fffffff : kFewRows;
+    p.min_blocks = 1;
+    p.wait_at_end = 0;
+    int r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
+    if (r != MOE_OK) return r;
+    launches += 1;
+    if (!only_few(s)) {
+        p.desc = reinterpret_cast<AttnDesc *>(ws + w.many_desc);
+        p.part = reinterpret_cast<float *>(ws + w.many_part);
+        p.min_rows = kFewRows + 1;
+        p.max_rows = 0x7fffffff;
+        p.wait_at_end = 1;
+        if (attn_tc_takes(s)) {
+            many = AttnParts{p.part, p.desc, attn_tc_ctas(), 256};
+            if (many.ctas == 0 || launch_attn_tc(p, kD, many.ctas, true, st) != cudaSuccess) return MOE_ERR_CUDA;
+        } else {
+            r = e4m3 ? launch_mma<kD, true, 4>(p, many, true, st) : launch_mma<kD, false, 4>(p, many, true, st);
+            if (r != MOE_OK) return r;
+        }
+        launches += 1;
+    }
+    const int rows = many.rows > few.rows ? many.rows : few.rows;
+    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas, (rows + 7) / 8), dim3(256), 0, st, true, p, few, many) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    launches += 1;
+    return MOE_OK;
 }
 
 static bool attn_misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
@@ -675,20 +741,6 @@ static int check_attn(const moe_attn_shape_t *shape)
     if (!(s.scale - s.scale == 0.0f)) return MOE_ERR_INVALID_ARG;          // not finite
     if (s.cache_dtype == MOE_E4M3 && (!(s.k_scale > 0.0f) || !(s.v_scale > 0.0f))) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
-}
-
-struct AttnWs {
-    size_t desc, part, total;
-};
-
-static AttnWs attn_ws(const moe_attn_shape_t &s)
-{
-    AttnWs w;
-    w.desc = 0;
-    w.part = (sizeof(AttnDesc) * kAttnMaxCtas + 255) / 256 * 256;
-    const size_t rows = s.max_q > 0 && static_cast<int64_t>(s.max_q) * (s.n_heads / s.n_kv_heads) <= 16 ? 16 : 64;
-    w.total = w.part + static_cast<size_t>(kAttnMaxCtas) * 2 * rows * (s.head_dim + 2) * 4;
-    return w;
 }
 
 }  // namespace moe
@@ -718,8 +770,7 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     if (attn_misaligned(q) || attn_misaligned(k_cache) || attn_misaligned(v_cache) || attn_misaligned(out) ||
         (reinterpret_cast<uintptr_t>(ws) & 255))
         return MOE_ERR_INVALID_ARG;
-    const AttnWs w = attn_ws(s);
-    if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < attn_ws(s).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     AttnParams p;
     p.q = q;
     p.k_cache = k_cache;
@@ -729,8 +780,6 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     p.kv_len = kv_len;
     p.out = out;
     p.status = status;
-    p.desc = reinterpret_cast<AttnDesc *>(static_cast<char *>(ws) + w.desc);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + w.part);
     p.q_stride = s.q_stride ? s.q_stride : static_cast<int64_t>(s.n_heads) * s.head_dim;
     p.page_stride = s.page_stride ? s.page_stride : static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim;
     p.B = s.B;
@@ -742,15 +791,12 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     p.num_pages = s.num_pages;
     p.max_pages = s.max_pages;
     p.causal = s.causal;
-    p.min_rows = 1;
-    p.max_rows = 0x7fffffff;
-    p.min_blocks = 1;
-    p.wait_at_end = 0;
     const bool e4m3 = s.cache_dtype == MOE_E4M3;
     p.scale_log2 = s.scale * (e4m3 ? s.k_scale : 1.0f) * 1.4426950408889634f;
     p.v_scale = e4m3 ? s.v_scale : 1.0f;
     cudaStream_t sm = reinterpret_cast<cudaStream_t>(stream);
-    if (s.head_dim == 64) return launch_for_dim<64>(s, p, sm, launches);
-    if (s.head_dim == 128) return launch_for_dim<128>(s, p, sm, launches);
-    return launch_for_dim<256>(s, p, sm, launches);
+    char *wb = static_cast<char *>(ws);
+    if (s.head_dim == 64) return launch_attention<64>(s, p, wb, sm, launches);
+    if (s.head_dim == 128) return launch_attention<128>(s, p, wb, sm, launches);
+    return launch_attention<256>(s, p, wb, sm, launches);
 }

@@ -20,6 +20,7 @@ namespace moe {
 
 constexpr int kAttnMaxB = 4096;
 constexpr int kAttnMaxCtas = 160 * 4;       // resident CTAs of one kernel, at most
+constexpr int kAttnTcMaxCtas = 160;         // the tensor-memory kernel has one per SM
 
 // What a combine block needs to know of the item that CTA c started and did not
 // finish: its parts are (c, slot 1), (c + 1, slot 0), ... (c + parts - 1, slot 0).
@@ -280,5 +281,11 @@ struct Split {
         return k;
     }
 };
+
+// The tensor-memory kernel: whether it takes a shape, its CTAs on this device (0
+// on an error), its launch.
+bool attn_tc_takes(const moe_attn_shape_t &s);
+int attn_tc_ctas();
+cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st);
 
 }  // namespace moe
