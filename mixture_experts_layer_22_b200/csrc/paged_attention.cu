@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             constexpr int kTpr = 128 / kRows, kCpt = kD / 8 / kTpr;   // threads per row, chunks per thread
             const int r = tid / kTpr, part = tid % kTpr;
             const int rows = cur.rows(p);
-            const int grow = cur.row0() + r;
+            const int grow = cur.row0(p) + r;
             const int tok = grow / p.group;
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
                                        static_cast<long long>(cur.r.qs + tok) * p.q_stride +
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = r_lo + 8 * h;
-                lim[h] = r < cur.rows(p) ? row_limit(p, cur.r, cur.row0() + r) : 0;
+                lim[h] = r < cur.rows(p) ? row_limit(p, cur.r, cur.row0(p) + r) : 0;
                 mult[h] = p.scale_log2 * (kE4m3 ? s_inv[r] : 1.0f);
             }
             if constexpr (C::kQReg) {
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                 for (int h = 0; h < 2; ++h) {
                     const int r = r_lo + 8 * h;
                     if (r < rows) {
-                        const int grow = cur.row0() + r;
+                        const int grow = cur.row0(p) + r;
                         if (whole) {
                             const float inv = l[h] > 0.0f ? p.v_scale / l[h] : l[h] == 0.0f ? 0.0f : l[h];
                             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                     const float *v = s_merge + r * kD + c;
                     if (whole) {
                         const float inv = lt > 0.0f ? p.v_scale / lt : lt == 0.0f ? 0.0f : lt;
-                        const int grow = cur.row0() + r;
+                        const int grow = cur.row0(p) + r;
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                              (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
                                               cur.kvh * p.group + grow % p.group) * kD + c;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                 d.parts = 0;
                 d.qs = cur.r.qs;
                 d.kvh = cur.kvh;
-                d.row0 = cur.row0();
+                d.row0 = cur.row0(p);
                 d.rows = rows;
                 if (!last && !continued) d.parts = split.parts(blockIdx.x, item_from, cur.nblk);
                 p.desc[blockIdx.x] = d;
@@ -579,44 +579,45 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams
     const int c = second ? blockIdx.x - few.ctas : blockIdx.x;
     const int kRows = second ? many.rows : few.rows;
     const float *parts = second ? many.part : few.part;
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (r >= kRows) return;
+    const int lane = threadIdx.x & 31;
     grid_dep_wait();
     const AttnDesc d = second ? many.desc[c] : few.desc[c];
-    if (d.parts < 2 || r >= d.rows) return;
+    if (d.parts < 2) return;
     const long long stride = static_cast<long long>(kRows) * (kD + 2);
     // part k of the item
     auto part = [&](int k) { return parts + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
-    float mx = -INFINITY;
-    for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, part(k)[kRows * kD + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    float acc[kE], l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
-    for (int k = 0; k < d.parts; ++k) {
-        const float *q = part(k);
-        const float f = exp2_fast(q[kRows * kD + r] - base);
-        l += f * q[kRows * kD + kRows + r];
-        float v[kE];
-        if constexpr (kE == 2) {
-            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + r * kD + lane * kE);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kE; e += 4)
-                *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + r * kD + lane * kE + e);
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += 8 * gridDim.y) {
+        float mx = -INFINITY;
+        for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, part(k)[kRows * kD + r]);
+    #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float acc[kE], l = 0.0f;
+    #pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+        for (int k = 0; k < d.parts; ++k) {
+            const float *q = part(k);
+            const float f = exp2_fast(q[kRows * kD + r] - base);
+            l += f * q[kRows * kD + kRows + r];
+            float v[kE];
+            if constexpr (kE == 2) {
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + r * kD + lane * kE);
+            } else {
+    #pragma unroll
+                for (int e = 0; e < kE; e += 4)
+                    *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + r * kD + lane * kE + e);
+            }
+    #pragma unroll
+            for (int e = 0; e < kE; ++e) acc[e] += f * v[e];
         }
-#pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] += f * v[e];
+        const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
+        const int grow = d.row0 + r;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                             (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
+                             lane * kE;
+    #pragma unroll
+        for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
     }
-    const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
-    const int grow = d.row0 + r;
-    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                         (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
-                         lane * kE;
-#pragma unroll
-    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // CTAs of a kernel that are resident on the GPU at once, found once per kernel
@@ -679,7 +680,7 @@ static AttnWs attn_ws(const moe_attn_shape_t &s)
     w.few_part = 2 * w.many_desc;
     w.many_part = w.few_part + parts(kAttnMaxCtas, kFewRows);
     w.total = w.many_part;
-    if (!only_few(s)) w.total += attn_tc_takes(s) ? parts(kAttnTcMaxCtas, 256) : parts(kAttnMaxCtas, 64);
+    if (!only_few(s)) w.total += attn_tc_takes(s) ? parts(kAttnTcMaxCtas, attn_tc_rows(s)) : parts(kAttnMaxCtas, 64);
     return w;
 }
 
@@ -695,6 +696,7 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
     p.max_rows = only_few(s) ? 0x7fffffff : kFewRows;
     p.min_blocks = 1;
     p.wait_at_end = 0;
+    p.tile_rows = kFewRows;
     int r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
     if (r != MOE_OK) return r;
     launches += 1;
@@ -705,16 +707,18 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         p.max_rows = 0x7fffffff;
         p.wait_at_end = 1;
         if (attn_tc_takes(s)) {
-            many = AttnParts{p.part, p.desc, attn_tc_ctas(), 256};
+            p.tile_rows = attn_tc_rows(s);
+            many = AttnParts{p.part, p.desc, attn_tc_ctas(), p.tile_rows};
             if (many.ctas == 0 || launch_attn_tc(p, kD, many.ctas, true, st) != cudaSuccess) return MOE_ERR_CUDA;
         } else {
+            p.tile_rows = 64;
             r = e4m3 ? launch_mma<kD, true, 4>(p, many, true, st) : launch_mma<kD, false, 4>(p, many, true, st);
             if (r != MOE_OK) return r;
         }
         launches += 1;
     }
-    const int rows = many.rows > few.rows ? many.rows : few.rows;
-    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas, (rows + 7) / 8), dim3(256), 0, st, true, p, few, many) !=
+    // a warp has one row of a 16-row item, 8 of a 256-row one
+    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas, many.ctas ? 4 : 2), dim3(256), 0, st, true, p, few, many) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
     launches += 1;

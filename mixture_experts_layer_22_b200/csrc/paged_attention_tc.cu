@@ -12,15 +12,21 @@
 //     products of the other;
 //   - one thread per query row: a warpgroup owns a tile, a thread reads its row
 //     of S from tensor memory, and no value crosses threads;
+//   - a block is worked on in two halves of 64 keys with their own columns of S:
+//     the scores of one half are made while the softmax of the other runs, so the
+//     softmax never waits for its own products;
 //   - P (bf16) takes the place of S in tensor memory and is the A operand of the
 //     second product from there: it never goes through shared memory;
 //   - O stays in tensor memory.  Its rows are rescaled only when their maximum
 //     has grown by more than 2^8 since the last time (until then p may exceed 1,
 //     which costs nothing in bf16 and in fp32 sums).
-// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1 (they also bring Q into shared
-// memory and write the output), 8 issues the MMAs, 9 the TMA loads, 10 and 11 fill
-// their warpgroup up, which hands registers to the softmax: a thread there holds
-// its row's 128 scores.  K and V
+//   - an item's Q is loaded as soon as the last scores of the item before are
+//     done, and its first scores are issued behind that item's last products, so
+//     that they run while its output is written.
+// A tile holds whole tokens: tile_rows / 2 = group * floor(128 / group) rows.
+// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1 and the output, 8 and 11 issue
+// the MMAs of tile 0 and 1 (apart, because a wait of one must not hold up the
+// other), 9 loads K and V, 10 loads Q.  K and V
 // blocks share one ring of slots in the order K0 V0 K1 V1 ...; a block is put
 // together from one TMA box per page and 64 columns, whose page ids the 32 lanes
 // of the load warp read side by side.
@@ -36,7 +42,7 @@ namespace moe {
 
 template <int kD>
 struct TcCfg {
-    static constexpr int kThreads = 384, kRows = 256, kBlk = 128;
+    static constexpr int kThreads = 384, kBlk = 128;
     static constexpr int kHalf = 128 * 128;                  // bytes of 128 rows x 64 columns
     static constexpr int kHalves = kD / 64;
     static constexpr int kTile = kHalves * kHalf;            // 128 rows x D
@@ -46,6 +52,40 @@ struct TcCfg {
 };
 
 constexpr float kRescale = 8.0f;                             // log2 of the growth that is let stand
+
+// One lane of a converged warp.  Code under it is known to the compiler to run in
+// one thread, which tcgen05 instructions want (their operands are uniform
+// registers): under a plain test of the lane each MMA took some 100 cycles to issue.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// Bounded wait for the phase of the given parity, as mbar_wait, but the wall
+// clock is read only every 256 tries: a wait here is on the critical path of
+// every block, and reading the clock takes longer than the phase.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kTimeoutNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
 
 // Shared-memory descriptor of an operand stored with its M or N dimension
 // contiguous, 128-byte swizzle: 64-element blocks `lead` bytes apart along that
@@ -118,26 +158,29 @@ __device__ __forceinline__ float tc_exp2(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t tc_bf16x2(float a, float b)
 {
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Geometry of the cache's tensor maps: box_rows rows of a page per TMA box.
-struct TcMaps {
-    int box_rows;
-};
-
 template <int kD>
 __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
-    paged_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                              const AttnParams p, const TcMaps maps)
+    paged_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                              const __grid_constant__ CUtensorMap tm_v, const AttnParams p, int box_rows)
 {
     using C = TcCfg<kD>;
-    constexpr int kRows = C::kRows, kBlk = C::kBlk, kSlots = C::kSlots;
+    constexpr int kBlk = C::kBlk, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_full[kSlots], s_empty[kSlots], s_qfull[2], s_sfull[2], s_pfull[2], s_ofull[2], s_drain;
+    __shared__ uint64_t s_full[kSlots], s_empty[kSlots], s_qfull[2], s_qempty[2], s_sfull[2][2], s_pfull[2][2],
+        s_pv[2][2], s_drain[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -148,20 +191,23 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&s_empty[i]), 1);
+            mbar_init(smem_u32(&s_empty[i]), 2);             // both tiles
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(smem_u32(&s_qfull[t]), 4);
-            mbar_init(smem_u32(&s_sfull[t]), 1);
-            mbar_init(smem_u32(&s_pfull[t]), 4);
-            mbar_init(smem_u32(&s_ofull[t]), 1);
+            mbar_init(smem_u32(&s_qfull[t]), 1);
+            mbar_init(smem_u32(&s_qempty[t]), 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(smem_u32(&s_sfull[t][x]), 1);
+                mbar_init(smem_u32(&s_pfull[t][x]), 4);
+                mbar_init(smem_u32(&s_pv[t][x]), 1);
+            }
+            mbar_init(smem_u32(&s_drain[t]), 1);
         }
-        mbar_init(smem_u32(&s_drain), 1);
         s_abort = 0;
         fence_mbar_init();
     }
-    Split<C::kThreads, kRows, kBlk> split;
-    Cursor<kRows, kBlk> cur;
+    Split<C::kThreads, 0, kBlk> split;
+    Cursor<0, kBlk> cur;
     const long long n_blocks = split.init(p, cur);           // ends with a block barrier
     grid_dep_launch();
     if (n_blocks == 0) {
@@ -179,23 +225,50 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
     const uint32_t tmem = s_tmem;
     // a wait's answer is the whole warp's
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, &s_abort));
+        return __all_sync(0xffffffffu, tc_wait(smem_u32(bar), parity, &s_abort));
     };
+    const int tile = p.tile_rows >> 1;                       // rows of a tile, at most 128
     long long left = n_blocks;
     // 12 warps x 168 registers at launch = 8 x 216 + 4 x 72
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 9) {
-        // ---------------------------------------------------------- TMA loads
+    if (warp == 10) {
+        // ------------------------------------------------------------ Q loads
+        uint32_t n_fill[2] = {0, 0};
+        bool ok = true;
+        const uint64_t policy = policy_evict_normal();
+        while (left > 0 && ok) {
+            const int rows = cur.rows(p), tok = cur.r.qs + cur.row0(p) / p.group;
+            for (int t = 0; t < 2 && t * tile < rows && ok; ++t) {
+                ok = wait(&s_qempty[t], (n_fill[t] & 1u) ^ 1u);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&s_qfull[t]);
+                    mbar_arrive_expect_tx(bar, C::kHalves * tile * 128);
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_3d(smem_u32(s_q) + t * C::kTile + h * C::kHalf, &tm_q, bar, 64 * h, cur.kvh * p.group,
+                                    tok + t * (tile / p.group), policy);
+                }
+                __syncwarp();
+                ++n_fill[t];
+            }
+            left -= min(left, static_cast<long long>(cur.nblk - cur.blk));
+            if (left > 0) cur.next_item(p);
+        }
+        volatile int no_abort = 0;                           // the last copies land before the CTA leaves
+        for (int t = 0; t < 2 && !ok; ++t)
+            if (n_fill[t]) mbar_wait(smem_u32(&s_qfull[t]), (n_fill[t] - 1) & 1u, &no_abort);
+    } else if (warp == 9) {
+        // ---------------------------------------------------- K and V loads
         // lane: box of rows row .. row + box_rows - 1 of the block, columns 64 h ..
-        const int boxes = kBlk / maps.box_rows;
-        const int h = lane / boxes, row = lane % boxes * maps.box_rows;
+        const int boxes = kBlk / box_rows;
+        const int h = lane / boxes, row = lane % boxes * box_rows;
         const bool mine = h < C::kHalves;
         const uint64_t policy = policy_evict_normal();
         bool bad = false;
         int slot = 0;
         uint32_t phase = 0, n_fill = 0;
-        auto page_of = [&](const Cursor<kRows, kBlk> &at) {  // -1: no such key
+        auto page_of = [&](const Cursor<0, kBlk> &at) {  // -1: no such key
             const int key = at.blk * kBlk + row;
             if (!mine || key >= at.r.kv) return -1;
             int id = __ldg(p.table + static_cast<long long>(at.b) * p.max_pages + key / p.page_size);
@@ -221,7 +294,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                 ok = wait(&s_empty[slot], phase ^ 1u);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[slot]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, n_box * maps.box_rows * 128);
+                if (lane == 0) mbar_arrive_expect_tx(bar, n_box * box_rows * 128);
                 __syncwarp();
                 if (id >= 0)
                     tma_load_4d(ring + slot * C::kTile + h * C::kHalf + row * 128, kv ? &tm_v : &tm_k, bar, 64 * h, kvh, off, id,
@@ -242,99 +315,110 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
             for (uint32_t i = n_fill > kSlots ? n_fill - kSlots : 0; i < n_fill; ++i)
                 mbar_wait(smem_u32(&s_full[i % kSlots]), (i / kSlots) & 1u, &no_abort);
         }
-    } else if (warp == 8) {
-        // --------------------------------------------------------------- MMAs
-        const uint32_t idesc_s = idesc_make(1, 128, 128), idesc_o = idesc_make(1, 128, kD) | (1u << 16);
-        const uint32_t q0 = smem_u32(s_q);
-        int slot = 0;
-        uint32_t phase = 0, qphase[2] = {0, 0}, pphase[2] = {0, 0};
+    } else {
+        // ------------------------------------------------- MMAs of tile t
+        const int t = warp == 8 ? 0 : 1;
+        const uint32_t idesc_s = idesc_make(1, 128, 64), idesc_o = idesc_make(1, 128, kD) | (1u << 16);
+        const uint32_t q0 = smem_u32(s_q) + t * C::kTile;
+        const uint32_t ts = tmem + C::kColS + 128 * t, to = tmem + C::kColO + 128 * t;
+        int slot = 0;                                        // the next fill to wait for
+        uint32_t phase = 0, qphase = 0, pphase = 0;
         bool ok = true;
-        auto scores = [&](int t, int kslot) {
-            if (lane == 0) {
-                const uint32_t a = q0 + t * C::kTile, b = ring + kslot * C::kTile;
-#pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    const uint32_t at = (ks >> 2) * C::kHalf + (ks & 3) * 32;
-                    mma_bf16(tmem + C::kColS + 128 * t, sdesc_k_sw128(a + at), sdesc_k_sw128(b + at), idesc_s, ks > 0);
-                }
-                mma_commit(smem_u32(&s_sfull[t]));
-            }
-        };
-        auto next_slot = [&]() {
+        auto next_fill = [&]() {                             // its slot, once it has landed
+            ok = wait(&s_full[slot], phase);
+            const int x = slot;
             if (++slot == kSlots) {
                 slot = 0;
                 phase ^= 1u;
             }
+            return x;
+        };
+        auto scores = [&](int kslot, int half) {             // S half = Q K[64 half ..]^T
+            if (elect_one()) {
+                const uint32_t b = ring + kslot * C::kTile + half * 8192;
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    const uint32_t at = (ks >> 2) * C::kHalf + (ks & 3) * 32;
+                    mma_bf16(ts + 64 * half, sdesc_k_sw128(q0 + at), sdesc_k_sw128(b + at), idesc_s, ks > 0);
+                }
+                mma_commit(smem_u32(&s_sfull[t][half]));
+            }
         };
         while (left > 0 && ok) {
             const int n = static_cast<int>(min(left, static_cast<long long>(cur.nblk - cur.blk)));
-            const int tiles = cur.rows(p) > 128 ? 2 : 1;
-            ok = wait(&s_full[slot], phase);
-            for (int t = 0; t < tiles && ok; ++t) {
-                ok = wait(&s_qfull[t], qphase[t]);
+            if (t * tile < cur.rows(p)) {
+                int kslot = next_fill();
                 if (!ok) break;
-                qphase[t] ^= 1u;
+                ok = wait(&s_qfull[t], qphase);
+                if (!ok) break;
+                qphase ^= 1u;
                 tc_fence_after();
-                scores(t, slot);
+                scores(kslot, 0);
+                scores(kslot, 1);
+                if (elect_one()) {
+                    mma_commit(smem_u32(&s_empty[kslot]));
+                    if (n == 1) mma_commit(smem_u32(&s_qempty[t]));
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const int vslot = next_fill();
+                    if (!ok) break;
+                    // values behind the last key must not reach the product: 0 x NaN
+                    // (both tiles' warps write the same zeros)
+                    const int valid = cur.r.kv - (cur.blk + j) * kBlk;
+                    if (valid < kBlk) {
+                        uint8_t *v = smem + 2 * C::kTile + vslot * C::kTile;
+                        const int from = valid < 0 ? 0 : valid;
+                        for (int x = from * 8 + lane; x < kBlk * 8; x += 32)
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; ++h)
+                                *reinterpret_cast<uint4 *>(v + h * C::kHalf + x * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = wait(&s_pfull[t][half], pphase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t b = ring + vslot * C::kTile + half * 8192;
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ta(to, ts + 64 * half + 8 * ks, sdesc_mn_sw128(b + ks * 2048, C::kHalf), idesc_o,
+                                           j > 0 || half > 0 || ks > 0);
+                            mma_commit(smem_u32(&s_pv[t][half]));
+                            if (half == 1) mma_commit(smem_u32(&s_empty[vslot]));
+                        }
+                        if (j + 1 < n) {
+                            if (half == 0) {
+                                kslot = next_fill();
+                                if (!ok) break;
+                            }
+                            scores(kslot, half);
+                            if (half == 1 && elect_one()) {
+                                mma_commit(smem_u32(&s_empty[kslot]));
+                                if (j + 2 == n) mma_commit(smem_u32(&s_qempty[t]));
+                            }
+                        }
+                    }
+                    pphase ^= 1u;
+                }
+            } else {
+                // no rows for this tile: only give the slots back
+                for (int x = 0; x < 2 * n && ok; ++x) {
+                    const int f = next_fill();
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&s_empty[f]));
+                }
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(smem_u32(&s_empty[slot]));
-            next_slot();
-            for (int j = 0; j < n && ok; ++j) {
-                const int vslot = slot;
-                ok = wait(&s_full[slot], phase);
-                if (!ok) break;
-                next_slot();
-                // values behind the last key must not reach the product: 0 x NaN
-                const int valid = cur.r.kv - (cur.blk + j) * kBlk;
-                if (valid < kBlk) {
-                    uint8_t *v = smem + 2 * C::kTile + vslot * C::kTile;
-                    const int from = valid < 0 ? 0 : valid;
-                    for (int x = from * 8 + lane; x < kBlk * 8; x += 32)
-#pragma unroll
-                        for (int h = 0; h < C::kHalves; ++h)
-                            *reinterpret_cast<uint4 *>(v + h * C::kHalf + x * 16) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                const int kslot = slot;
-                for (int t = 0; t < tiles && ok; ++t) {
-                    ok = wait(&s_pfull[t], pphase[t]);
-                    if (!ok) break;
-                    pphase[t] ^= 1u;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t b = ring + vslot * C::kTile;
-#pragma unroll
-                        for (int ks = 0; ks < kBlk / 16; ++ks)
-                            mma_f16_ta(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + 8 * ks,
-                                       sdesc_mn_sw128(b + ks * 2048, C::kHalf), idesc_o, j > 0 || ks > 0);
-                    }
-                    if (j + 1 < n) {
-                        if (t == 0) {
-                            ok = wait(&s_full[slot], phase);
-                            if (!ok) break;
-                        }
-                        scores(t, kslot);
-                    } else if (lane == 0) {
-                        mma_commit(smem_u32(&s_ofull[t]));
-                    }
-                }
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(smem_u32(&s_empty[vslot]));
-                    if (j + 1 < n) mma_commit(smem_u32(&s_empty[kslot]));
-                }
-                if (j + 1 < n) next_slot();
-            }
             left -= n;
             if (left > 0) cur.next_item(p);
         }
         if (!ok) {
-            if (lane == 0) {
+            if (elect_one()) {
                 volatile int no_abort = 0;
-                mma_commit(smem_u32(&s_drain));
-                mbar_wait(smem_u32(&s_drain), 0, &no_abort);
+                mma_commit(smem_u32(&s_drain[t]));
+                mbar_wait(smem_u32(&s_drain[t]), 0, &no_abort);
             }
             __syncwarp();
         }
@@ -345,66 +429,55 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // lane 32 (warp mod 4) in bits 16..
         const uint32_t ts = tmem + C::kColS + 128 * t + lanes, to = tmem + C::kColO + 128 * t + lanes;
-        const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;      // a negative scale: -q and its magnitude
-        const float mult = fmaxf(fabsf(p.scale_log2), 1e-30f);             // 0 times a masked -inf must stay -inf
-        uint32_t sphase = 0, ophase = 0;
+        const float mult = fmaxf(p.scale_log2, 1e-30f);                    // 0 times a masked -inf must stay -inf
+        uint32_t ph = 0;                                     // of the barriers of the block's two halves
         bool ok = true, continued = cur.blk > 0;
         long long item_from = 0;
         while (left > 0 && ok) {
             const int n = static_cast<int>(min(left, static_cast<long long>(cur.nblk - cur.blk)));
             const bool last = cur.blk + n == cur.nblk;
             const int rows = cur.rows(p);
-            if (128 * t < rows) {
-                const int row = 128 * t + r, grow = cur.row0() + row;
-                const bool real = row < rows;
+            if (t * tile < rows) {
+                const int row = t * tile + r, grow = cur.row0(p) + row;
+                const bool real = r < tile && row < rows;
                 const long long tok = cur.r.qs + grow / p.group;
                 const int head = cur.kvh * p.group + grow % p.group;
                 const int lim = real ? row_limit(p, cur.r, grow) : 0;
-                {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + tok * p.q_stride +
-                                                                       static_cast<long long>(head) * kD);
-                    uint8_t *dst = s_q + t * C::kTile + r * 128;
-#pragma unroll
-                    for (int c = 0; c < kD / 8; ++c) {
-                        uint4 w = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                        w.x ^= flip;
-                        w.y ^= flip;
-                        w.z ^= flip;
-                        w.w ^= flip;
-                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kHalf + ((c & 7) ^ (r & 7)) * 16) = w;
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_qfull[t]));
-                }
                 float m = -INFINITY, l = 0.0f;               // m: largest q.k that O is relative to
-                for (int j = 0; j < n; ++j) {
-                    ok = wait(&s_sfull[t], sphase);
+                for (int x = 0; x < 2 * n; ++x) {            // blocks of 64 keys
+                    const int half = x & 1;
+                    ok = wait(&s_sfull[t][half], ph);
                     if (!ok) break;
-                    sphase ^= 1u;
                     tc_fence_after();
-                    float s[kBlk];
-#pragma unroll
-                    for (int c = 0; c < kBlk; c += 32) tmem_ld32(ts + c, s + c);
+                    float s[64];
+                    tmem_ld32(ts + 64 * half, s);
+                    tmem_ld32(ts + 64 * half + 32, s + 32);
                     tmem_wait_ld();
-                    const int seen = lim - (cur.blk + j) * kBlk;
-                    if (__any_sync(0xffffffffu, seen < kBlk)) {
+                    const int seen = lim - (cur.blk * kBlk + 64 * x);
+                    const bool masked = __any_sync(0xffffffffu, seen < 64);
+                    if (masked) {
 #pragma unroll
-                        for (int i = 0; i < kBlk; ++i) s[i] = i < seen ? s[i] : -INFINITY;
+                        for (int i = 0; i < 64; ++i) s[i] = i < seen ? s[i] : -INFINITY;
                     }
-                    float top[4] = {s[0], s[1], s[2], s[3]};
+                    float top[8];
 #pragma unroll
-                    for (int i = 4; i < kBlk; i += 8)
+                    for (int e = 0; e < 8; ++e) top[e] = max3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top[e] = i + 4 + e < kBlk ? fmaxf(fmaxf(top[e], s[i + e]), s[i + 4 + e]) : fmaxf(top[e], s[i + e]);
-                    const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    for (int i = 24; i < 56; i += 16)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top[e] = max3(top[e], s[i + e], s[i + 8 + e]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top[e] = fmaxf(top[e], s[56 + e]);
+                    const float mn = max3(max3(m, top[0], top[1]), max3(top[2], top[3], top[4]), max3(top[5], top[6], top[7]));
                     if (__any_sync(0xffffffffu, (mn - m) * mult > kRescale)) {
                         // (mn = m = -inf gives NaN above and does not count)
                         const float f = m == -INFINITY ? 0.0f : tc_exp2((m - mn) * mult);
                         m = mn;
                         l *= f;
-                        if (j > 0) {
+                        if (x > 0) {
+                            ok = wait(&s_pv[t][half ^ 1], half ? ph : ph ^ 1u);      // O at rest
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
                             for (int c = 0; c < kD; c += 32) {
                                 float o[32];
@@ -417,28 +490,27 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                         }
                     }
                     const float base = m == -INFINITY ? 0.0f : m * mult;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    uint32_t w[32];
+                    const float2 mult2 = make_float2(mult, mult), base2 = make_float2(-base, -base);
 #pragma unroll
-                    for (int c = 0; c < kBlk; c += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float a = tc_exp2(fmaf(s[c + i], mult, -base)), b = tc_exp2(fmaf(s[c + i + 1], mult, -base));
-                            sum[i & 2] += a;
-                            sum[(i & 2) + 1] += b;
-                            w[i >> 1] = tc_bf16x2(a, b);
-                        }
-                        tmem_st16(ts + (c >> 1), w);
+                    for (int i = 0; i < 64; i += 2) {
+                        const float2 v = __ffma2_rn(make_float2(s[i], s[i + 1]), mult2, base2);
+                        const float2 e = make_float2(tc_exp2(v.x), tc_exp2(v.y));
+                        sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
+                        w[i >> 1] = tc_bf16x2(e.x, e.y);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st16(ts + 64 * half, w);
+                    tmem_st16(ts + 64 * half + 16, w + 16);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_pfull[t]));
+                    if (lane == 0) mbar_arrive(smem_u32(&s_pfull[t][half]));
+                    ph ^= half;
                 }
-                if (ok) ok = wait(&s_ofull[t], ophase);
+                if (ok) ok = wait(&s_pv[t][1], ph ^ 1u);
                 if (!ok) break;
-                ophase ^= 1u;
                 tc_fence_after();
                 if (last && !continued) {
                     const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
@@ -457,7 +529,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                         }
                     }
                 } else {
-                    float *part = p.part + (2LL * blockIdx.x + (continued ? 0 : 1)) * (kRows * (kD + 2));
+                    float *part = p.part + (2LL * blockIdx.x + (continued ? 0 : 1)) * (static_cast<long long>(p.tile_rows) * (kD + 2));
 #pragma unroll
                     for (int c = 0; c < kD; c += 32) {
                         float o[32];
@@ -470,8 +542,8 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                         }
                     }
                     if (real) {
-                        part[kRows * kD + row] = m == -INFINITY ? m : m * mult;
-                        part[kRows * kD + kRows + row] = l;
+                        part[p.tile_rows * kD + row] = m == -INFINITY ? m : m * mult;
+                        part[p.tile_rows * (kD + 1) + row] = l;
                     }
                 }
                 tc_fence_before();
@@ -483,7 +555,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                     d.parts = 0;
                     d.qs = cur.r.qs;
                     d.kvh = cur.kvh;
-                    d.row0 = cur.row0();
+                    d.row0 = cur.row0(p);
                     d.rows = rows;
                     if (!last && !continued) d.parts = split.parts(blockIdx.x, item_from, cur.nblk);
                     p.desc[blockIdx.x] = d;
@@ -526,29 +598,54 @@ static AttnEncodeFn attn_encode_fn()
     return fn;
 }
 
+static bool encode_bf16(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                        const cuuint32_t *box)
+{
+    AttnEncodeFn fn = attn_encode_fn();
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A cache as [num_pages][page_size][n_kv][D] with boxes of box_rows tokens of one
 // head and 64 columns.
 static bool cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, int box_rows)
 {
-    AttnEncodeFn fn = attn_encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_kv), static_cast<cuuint64_t>(p.page_size),
                                 static_cast<cuuint64_t>(p.num_pages)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(kD) * 2 * p.n_kv,
                                    static_cast<cuuint64_t>(p.page_stride) * 2};
-    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1}, one[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+    return encode_bf16(m, base, 4, dims, strides, box);
+}
+
+// Queries as [T][n_heads][D] with boxes of a tile's tokens, one group's heads and
+// 64 columns: a tile's rows in their order.
+static bool query_map(CUtensorMap *m, const AttnParams &p, int kD)
+{
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_heads), static_cast<cuuint64_t>(p.T)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
+    return encode_bf16(m, p.q, 3, dims, strides, box);
 }
 
 bool attn_tc_takes(const moe_attn_shape_t &s)
 {
     // a block of 128 keys is made of whole boxes: pages that divide it (the
-    // 1024-byte swizzle pattern wants at least 8 rows), or that it divides.  A
-    // tensor map's stride is below 2^40 bytes.
+    // 1024-byte swizzle pattern wants at least 8 rows), or that it divides; a
+    // tile of 128 rows holds whole tokens; and the maximum of q.k is that of the
+    // scores.  A tensor map's strides are below 2^40 bytes.
     if (s.head_dim != 64 && s.head_dim != 128) return false;
-    if (s.cache_dtype != MOE_BF16) return false;
+    if (s.cache_dtype != MOE_BF16 || s.n_heads / s.n_kv_heads > 128 || s.scale < 0.0f) return false;
+    if (s.q_stride >= 1ll << 39 || s.page_stride >= 1ll << 39) return false;
     return (s.page_size >= 8 && 128 % s.page_size == 0) || s.page_size % 128 == 0;
+}
+
+int attn_tc_rows(const moe_attn_shape_t &s)
+{
+    const int group = s.n_heads / s.n_kv_heads;
+    return 2 * group * (128 / group);
 }
 
 int attn_tc_ctas()
@@ -572,16 +669,16 @@ int attn_tc_ctas()
 
 cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st)
 {
-    TcMaps maps;
-    maps.box_rows = p.page_size < 128 ? p.page_size : 128;
-    CUtensorMap k, v;
-    if (!cache_map(&k, p.k_cache, p, head_dim, maps.box_rows) || !cache_map(&v, p.v_cache, p, head_dim, maps.box_rows))
+    const int box_rows = p.page_size < 128 ? p.page_size : 128;
+    CUtensorMap q, k, v;
+    if (!query_map(&q, p, head_dim) || !cache_map(&k, p.k_cache, p, head_dim, box_rows) ||
+        !cache_map(&v, p.v_cache, p, head_dim, box_rows))
         return cudaErrorInvalidValue;
     if (head_dim == 64)
-        return launch_kernel(paged_attention_tc_kernel<64>, dim3(ctas), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, k, v, p,
-                             maps);
-    return launch_kernel(paged_attention_tc_kernel<128>, dim3(ctas), dim3(TcCfg<128>::kThreads), TcCfg<128>::kSmem, st, chained, k, v, p,
-                         maps);
+        return launch_kernel(paged_attention_tc_kernel<64>, dim3(ctas), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, q, k, v,
+                             p, box_rows);
+    return launch_kernel(paged_attention_tc_kernel<128>, dim3(ctas), dim3(TcCfg<128>::kThreads), TcCfg<128>::kSmem, st, chained, q, k, v, p,
+                         box_rows);
 }
 
 }  // namespace moe

@@ -39,6 +39,7 @@ struct AttnParams {
     long long q_stride, page_stride;
     int B, T, n_heads, n_kv, group, page_size, num_pages, max_pages, causal;
     int min_rows, max_rows;   // this kernel's requests: rows in [min_rows, max_rows]
+    int tile_rows;            // query rows of an item
     int min_blocks;           // a CTA gets at least this many blocks
     int wait_at_end;          // launched while the kernel before it runs
     float scale_log2, v_scale;
@@ -113,20 +114,27 @@ __device__ __forceinline__ long long floor_sum(long long m, long long c, long lo
     }
 }
 
+// Query rows of an item: the kernel's constant, or p.tile_rows where kRows is 0.
+template <int kRows>
+__device__ __forceinline__ int item_rows(const AttnParams &p)
+{
+    return kRows > 0 ? kRows : p.tile_rows;
+}
+
 // Blocks of one request and key/value head, all tiles.
 template <int kRows, int kBlk>
 __device__ __forceinline__ long long request_blocks(const AttnParams &p, const Req &r)
 {
     if (r.n == 0) return 0;
-    const int rows = r.n * p.group, tiles = (rows + kRows - 1) / kRows;
+    const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = (rows + per - 1) / per;
     if (!p.causal) return static_cast<long long>(tiles) * tile_blocks<kBlk>(p, r, rows - 1);
     long long s = tile_blocks<kBlk>(p, r, rows - 1);
-    if (kRows % p.group == 0 && r.kv >= r.n) {
-        // the full tiles see kv - n + (i + 1) kRows / group keys
-        const int step = kRows / p.group;
+    if (per % p.group == 0 && r.kv >= r.n) {
+        // the full tiles see kv - n + (i + 1) per / group keys
+        const int step = per / p.group;
         if (tiles > 1) s += floor_sum(tiles - 1, kBlk, step, r.kv - r.n + step + kBlk - 1);
     } else {
-        for (int i = 0; i < tiles - 1; ++i) s += tile_blocks<kBlk>(p, r, (i + 1) * kRows - 1);
+        for (int i = 0; i < tiles - 1; ++i) s += tile_blocks<kBlk>(p, r, (i + 1) * per - 1);
     }
     return s;
 }
@@ -137,11 +145,15 @@ struct Cursor {
     Req r;
     int b, kvh, tile, blk, nblk, tiles;
 
-    __device__ __forceinline__ int row0() const { return tile * kRows; }
-    __device__ __forceinline__ int rows(const AttnParams &p) const { return min(kRows, r.n * p.group - tile * kRows); }
+    __device__ __forceinline__ int row0(const AttnParams &p) const { return tile * item_rows<kRows>(p); }
+    __device__ __forceinline__ int rows(const AttnParams &p) const { return min(item_rows<kRows>(p), r.n * p.group - row0(p)); }
     __device__ __forceinline__ void enter(const AttnParams &p)
     {
-        nblk = tile_blocks<kBlk>(p, r, min((tile + 1) * kRows, r.n * p.group) - 1);
+        nblk = tile_blocks<kBlk>(p, r, row0(p) + rows(p) - 1);
+    }
+    __device__ __forceinline__ void enter_request(const AttnParams &p)
+    {
+        tiles = (r.n * p.group + item_rows<kRows>(p) - 1) / item_rows<kRows>(p);
     }
     // On to the next item (warp-collective).  There must be one.
     __device__ __forceinline__ void next_item(const AttnParams &p)
@@ -163,7 +175,7 @@ struct Cursor {
                     }
                 }
                 r = attn_request(p, b, bad);
-                tiles = (r.n * p.group + kRows - 1) / kRows;
+                enter_request(p);
             }
         }
         enter(p);
@@ -185,8 +197,8 @@ struct Split {
         __shared__ long long s_warp[kThreads / 32];
         __shared__ int s_at[4];
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        const int per = (p.B + kThreads - 1) / kThreads;
-        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        const int chunk = (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
         bool bad = false;
         long long sum = 0;
         for (int b = b0; b < b1; ++b) sum += p.n_kv * request_blocks<kRows, kBlk>(p, attn_request(p, b, bad));
@@ -225,7 +237,7 @@ struct Split {
             }
             const int kvh = static_cast<int>(at / per_head);
             at -= per_head * kvh;
-            const int rows = r.n * p.group, tiles = (rows + kRows - 1) / kRows;
+            const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = (rows + per - 1) / per;
             int tile = 0;
             if (!p.causal) {
                 const int nb = tile_blocks<kBlk>(p, r, rows - 1);
@@ -234,8 +246,8 @@ struct Split {
             } else {
                 // the blocks before tile i, by a request cut to its first i
                 // tiles' tokens, or tile by tile
-                if (kRows % p.group == 0 && r.kv >= r.n) {
-                    const int step = kRows / p.group;
+                if (per % p.group == 0 && r.kv >= r.n) {
+                    const int step = per / p.group;
                     const long long base = r.kv - r.n + step + kBlk - 1;
                     int lo = 0, hi = tiles;           // before(lo) <= at < before(hi)
                     while (hi - lo > 1) {
@@ -247,7 +259,7 @@ struct Split {
                     if (lo > 0) at -= floor_sum(lo, kBlk, step, base);
                 } else {
                     for (;; ++tile) {
-                        const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * kRows, rows) - 1);
+                        const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * per, rows) - 1);
                         if (at < nb) break;
                         at -= nb;
                     }
@@ -265,7 +277,7 @@ struct Split {
             cur.tile = s_at[2];
             cur.blk = s_at[3];
             cur.r = attn_request(p, cur.b, bad);
-            cur.tiles = (cur.r.n * p.group + kRows - 1) / kRows;
+            cur.enter_request(p);
             cur.enter(p);
         }
         return n;
@@ -282,9 +294,10 @@ struct Split {
     }
 };
 
-// The tensor-memory kernel: whether it takes a shape, its CTAs on this device (0
-// on an error), its launch.
+// The tensor-memory kernel: whether it takes a shape, the query rows of its items,
+// its CTAs on this device (0 on an error), its launch.
 bool attn_tc_takes(const moe_attn_shape_t &s);
+int attn_tc_rows(const moe_attn_shape_t &s);
 int attn_tc_ctas();
 cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st);
 

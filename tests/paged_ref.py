@@ -108,7 +108,7 @@ class Batch:
     position that no request holds is NaN."""
 
     def __init__(self, q_lens, kv_lens, *, heads=8, kv_heads=2, dim=128, ps=16, causal=True, e4m3=False, seed=0,
-                 spread=2.0, pad_rows=0, interleaved_kv=False, qkv=False):
+                 spread=2.0, pad_rows=0, interleaved_kv=False, qkv=False, scale=None):
         g = torch.Generator().manual_seed(seed)
         self.q_lens, self.kv_lens = list(q_lens), list(kv_lens)
         self.heads, self.kv_heads, self.dim, self.ps, self.causal, self.e4m3 = heads, kv_heads, dim, ps, causal, e4m3
@@ -146,7 +146,7 @@ class Batch:
             self.q, self.q_stride = (torch.randn(self.T, heads, dim, generator=g) * spread).to(torch.bfloat16), 0
         self.q_start = torch.tensor([0] + list(np.cumsum(self.q_lens)), dtype=torch.int32)
         self.kv_len = torch.tensor(self.kv_lens, dtype=torch.int32)
-        self.scale = dim ** -0.5
+        self.scale = dim ** -0.5 if scale is None else scale
 
     def reference(self, u_p=None):
         if u_p is None:

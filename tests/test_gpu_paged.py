@@ -278,7 +278,8 @@ def test_attention_lengths(name, dim, e4m3):
     _check_attn(ref.Batch(q, kv, heads=4, kv_heads=2, dim=dim, e4m3=e4m3, pad_rows=2))
 
 
-@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 8), (8, 1), (28, 4), (12, 4), (16, 1), (24, 1), (10, 2)])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 8), (8, 1), (28, 4), (12, 4), (16, 1), (24, 1), (10, 2), (48, 1),
+                                             (130, 1)])
 @pytest.mark.parametrize("q,kv", [([1, 1, 1], [200, 31, 513]), ([9, 50, 1], [9, 170, 300])], ids=["decode", "chunks"])
 def test_attention_head_layouts(heads, kv_heads, q, kv):
     _check_attn(ref.Batch(q, kv, heads=heads, kv_heads=kv_heads, dim=64, seed=1))
@@ -293,7 +294,8 @@ def test_attention_page_sizes(ps):
 
 @pytest.mark.parametrize("kw", [dict(causal=False), dict(interleaved_kv=True), dict(qkv=True),
                                 dict(qkv=True, interleaved_kv=True, e4m3=True), dict(spread=30.0), dict(spread=30.0, e4m3=True),
-                                dict(spread=0.0), dict(spread=1e-30, e4m3=True)],
+                                dict(spread=0.0), dict(spread=1e-30, e4m3=True),
+                                dict(scale=-0.1), dict(scale=0.0), dict(scale=-0.1, e4m3=True)],
                          ids=lambda kw: ",".join(map(str, kw.items())))
 @pytest.mark.parametrize("max_q", [None, 0, 1, 1000])
 def test_attention_forms_and_hints(kw, max_q):
