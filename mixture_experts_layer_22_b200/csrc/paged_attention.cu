@@ -569,55 +569,86 @@ struct AttnParts {
 };
 
 // Joins the parts of the items that lie in several CTAs' ranges, of one or two
-// kernels: blockIdx.x is the CTA that started the item, a warp per row, kD / 32
-// elements a lane.
-template <int kD>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, const AttnParts few, const AttnParts many)
+// kernels.  A block has one item (by the CTA that started it) and 32 of its rows,
+// 16 for the first kernel: a warp takes kR rows side by side, kD / 32 elements a
+// lane.  The parts' maxima and totals are read by a lane each.
+template <int kD, int kR>
+__device__ __forceinline__ void combine_rows(const AttnParams &p, const AttnParts &from, int c, int row)
 {
     constexpr int kE = kD / 32;
-    const bool second = static_cast<int>(blockIdx.x) >= few.ctas;
-    const int c = second ? blockIdx.x - few.ctas : blockIdx.x;
-    const int kRows = second ? many.rows : few.rows;
-    const float *parts = second ? many.part : few.part;
     const int lane = threadIdx.x & 31;
-    grid_dep_wait();
-    const AttnDesc d = second ? many.desc[c] : few.desc[c];
-    if (d.parts < 2) return;
-    const long long stride = static_cast<long long>(kRows) * (kD + 2);
+    const AttnDesc d = from.desc[c];
+    if (d.parts < 2 || row >= d.rows) return;
+    const long long stride = static_cast<long long>(from.rows) * (kD + 2);
     // part k of the item
-    auto part = [&](int k) { return parts + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += 8 * gridDim.y) {
-        float mx = -INFINITY;
-        for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, part(k)[kRows * kD + r]);
-    #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        float acc[kE], l = 0.0f;
-    #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
-        for (int k = 0; k < d.parts; ++k) {
-            const float *q = part(k);
-            const float f = exp2_fast(q[kRows * kD + r] - base);
-            l += f * q[kRows * kD + kRows + r];
-            float v[kE];
-            if constexpr (kE == 2) {
-                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + r * kD + lane * kE);
-            } else {
-    #pragma unroll
-                for (int e = 0; e < kE; e += 4)
-                    *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + r * kD + lane * kE + e);
+    auto part = [&](int k) { return from.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
+    float base[kR], l[kR], acc[kR][kE];
+#pragma unroll
+    for (int j = 0; j < kR; ++j) {
+        base[j] = -INFINITY;
+        for (int k = lane; k < d.parts; k += 32) base[j] = fmaxf(base[j], row + j < d.rows ? part(k)[from.rows * kD + row + j] : -INFINITY);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) base[j] = fmaxf(base[j], __shfl_xor_sync(0xffffffffu, base[j], o));
+        if (base[j] == -INFINITY) base[j] = 0.0f;
+        l[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[j][e] = 0.0f;
+    }
+    for (int k0 = 0; k0 < d.parts; k0 += 32) {
+        float f[kR];
+#pragma unroll
+        for (int j = 0; j < kR; ++j) {
+            f[j] = 0.0f;
+            if (k0 + lane < d.parts && row + j < d.rows) {
+                const float *q = part(k0 + lane) + from.rows * kD + row + j;
+                f[j] = exp2_fast(q[0] - base[j]);
+                l[j] += f[j] * q[from.rows];
             }
-    #pragma unroll
-            for (int e = 0; e < kE; ++e) acc[e] += f * v[e];
         }
-        const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
-        const int grow = d.row0 + r;
+        const int n = min(32, d.parts - k0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float *q = part(k0 + k) + static_cast<long long>(row) * kD + lane * kE;
+#pragma unroll
+            for (int j = 0; j < kR; ++j) {
+                const float fk = __shfl_sync(0xffffffffu, f[j], k);
+                if (row + j >= d.rows) continue;             // the same for the whole warp
+                float v[kE];
+                if constexpr (kE == 2) {
+                    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + j * kD);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kE; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + j * kD + e);
+                }
+#pragma unroll
+                for (int e = 0; e < kE; ++e) acc[j][e] += fk * v[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kR; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
+        if (row + j >= d.rows) break;
+        const float inv = l[j] > 0.0f ? p.v_scale / l[j] : l[j] == 0.0f ? 0.0f : l[j];
+        const int grow = d.row0 + row + j;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                              (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
                              lane * kE;
-    #pragma unroll
-        for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
+#pragma unroll
+        for (int e = 0; e < kE; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[j][e] * inv, acc[j][e + 1] * inv);
     }
+}
+
+template <int kD>
+__global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, const AttnParts few, const AttnParts many)
+{
+    const int warp = threadIdx.x >> 5, per = (many.rows + 31) / 32;
+    grid_dep_wait();
+    const int x = static_cast<int>(blockIdx.x) - few.ctas;
+    if (x < 0) combine_rows<kD, 2>(p, few, blockIdx.x, 2 * warp);
+    else combine_rows<kD, 4>(p, many, x / per, x % per * 32 + 4 * warp);
 }
 
 // CTAs of a kernel that are resident on the GPU at once, found once per kernel
@@ -717,8 +748,7 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         }
         launches += 1;
     }
-    // a warp has one row of a 16-row item, 8 of a 256-row one
-    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas, many.ctas ? 4 : 2), dim3(256), 0, st, true, p, few, many) !=
+    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas * ((many.rows + 31) / 32)), dim3(256), 0, st, true, p, few, many) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
     launches += 1;

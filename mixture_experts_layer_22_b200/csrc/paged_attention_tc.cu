@@ -206,22 +206,27 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
         s_abort = 0;
         fence_mbar_init();
     }
-    Split<C::kThreads, 0, kBlk> split;
-    Cursor<0, kBlk> cur;
-    const long long n_blocks = split.init(p, cur);           // ends with a block barrier
-    grid_dep_launch();
-    if (n_blocks == 0) {
-        if (tid == 0) p.desc[blockIdx.x].parts = 0;
-        if (p.wait_at_end) grid_dep_wait();
-        return;
-    }
     if (warp == 8) {
         tmem_alloc(smem_u32(&s_tmem), 512);
         tmem_relinquish();
     }
+    if (tid == 32) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
     tc_fence_before();
-    __syncthreads();
+    Split<C::kThreads, 0, kBlk> split;
+    Cursor<0, kBlk> cur;
+    const long long n_blocks = split.init(p, cur);           // has block barriers
     tc_fence_after();
+    grid_dep_launch();
+    if (n_blocks == 0) {
+        if (tid == 0) p.desc[blockIdx.x].parts = 0;
+        if (warp == 8) tmem_dealloc(s_tmem, 512);
+        if (p.wait_at_end) grid_dep_wait();
+        return;
+    }
     const uint32_t tmem = s_tmem;
     // a wait's answer is the whole warp's
     auto wait = [&](uint64_t *bar, uint32_t parity) {

@@ -90,6 +90,13 @@ __device__ __forceinline__ int tile_blocks(const AttnParams &p, const Req &r, in
     return nb < 1 ? 1 : nb;
 }
 
+// a / b for a >= 0, b > 0.  Nearly always both fit 32 bits, where a division costs
+// a fifth of a 64-bit one, and a CTA's first load waits for several.
+__device__ __forceinline__ long long div_ll(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // sum over i < m of floor((a i + b) / c), a, b >= 0, c > 0, by the Euclid-like
 // reduction that swaps the roles of a and c.
 __device__ __forceinline__ long long floor_sum(long long m, long long c, long long a, long long b)
@@ -97,17 +104,19 @@ __device__ __forceinline__ long long floor_sum(long long m, long long c, long lo
     long long s = 0;
     for (;;) {
         if (a >= c) {
-            s += (m - 1) * m / 2 * (a / c);
-            a %= c;
+            const long long x = div_ll(a, c);
+            s += (m - 1) * m / 2 * x;
+            a -= x * c;
         }
         if (b >= c) {
-            s += m * (b / c);
-            b %= c;
+            const long long x = div_ll(b, c);
+            s += m * x;
+            b -= x * c;
         }
         const long long y = a * m + b;
         if (y < c) return s;
-        m = y / c;
-        b = y % c;
+        m = div_ll(y, c);
+        b = y - m * c;
         const long long t = c;
         c = a;
         a = t;
@@ -190,7 +199,7 @@ struct Split {
     long long W;          // blocks in all
     int G;                // CTAs that share them
 
-    __device__ __forceinline__ long long cta_start(int c) const { return W * c / G; }
+    __device__ __forceinline__ long long cta_start(int c) const { return div_ll(W * c, G); }
 
     __device__ __forceinline__ long long init(const AttnParams &p, Cursor<kRows, kBlk> &cur)
     {
@@ -218,7 +227,7 @@ struct Split {
             if (w < warp) before += s_warp[w];
             W += s_warp[w];
         }
-        const long long most = (W + p.min_blocks - 1) / p.min_blocks;
+        const long long most = div_ll(W + p.min_blocks - 1, p.min_blocks);
         G = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
         if (c >= G) return 0;
@@ -235,13 +244,13 @@ struct Split {
                 if (at < per_head * p.n_kv) break;
                 at -= per_head * p.n_kv;
             }
-            const int kvh = static_cast<int>(at / per_head);
+            const int kvh = static_cast<int>(div_ll(at, per_head));
             at -= per_head * kvh;
             const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = (rows + per - 1) / per;
             int tile = 0;
             if (!p.causal) {
                 const int nb = tile_blocks<kBlk>(p, r, rows - 1);
-                tile = static_cast<int>(at / nb);
+                tile = static_cast<int>(div_ll(at, nb));
                 at -= static_cast<long long>(tile) * nb;
             } else {
                 // the blocks before tile i, by a request cut to its first i
