@@ -21,10 +21,7 @@
 // arithmetic intensity the tensor pipe idles either way.
 #include <atomic>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
+#include "paged_mma.cuh"
 #include "paged_work.cuh"
 
 namespace moe {
@@ -40,58 +37,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-
-// d += a b, 16 x 8 x 16, in bf16 or (kHalf) fp16 with fp32 sums
-template <bool kHalf>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if constexpr (kHalf)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t bf16x2_of(float a, float b)
-{
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t f16x2_of(float a, float b)
-{
-    const __half2 r = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-// two E4M3 codes (the low 16 bits) as two fp16 values, exactly
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes)
-{
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
-    return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
-}
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Geometry of one kernel: kWM warps down the query rows (16 each), 4 / kWM
@@ -113,14 +58,6 @@ struct AttnCfg {
     static constexpr bool kSplitP = !kE4m3 && kWM == 1;
     static constexpr bool kQReg = kD <= 128;
 };
-
-// 16-byte chunk c of row r, permuted so that the 8 rows an ldmatrix reads at one
-// chunk lie in 8 different bank groups
-template <int kChunks>
-__device__ __forceinline__ int chunk_of(int r, int c)
-{
-    return kChunks >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-}
 
 template <int kD, bool kE4m3, int kWM>
 __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p)
@@ -227,11 +164,9 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
     for (long long it = 0; it < n_blocks; ++it) {
         cp_async_wait<kStages - 2>();
         if (fresh_item) {
-            // the item's query rows into shared memory.  For an E4M3 cache they
-            // become fp16 times a power of two that brings the row's largest
-            // magnitude to [2^14, 2^15): exact but for elements below 2^-28 of it,
-            // and the row's columns are permuted within 16 to the order in which
-            // ldmatrix delivers a row of bytes.
+            // the item's query rows into shared memory; for an E4M3 cache in fp16
+            // (see row_power), the columns permuted within 16 to the order in
+            // which ldmatrix delivers a row of bytes
             constexpr int kTpr = 128 / kRows, kCpt = kD / 8 / kTpr;   // threads per row, chunks per thread
             const int r = tid / kTpr, part = tid % kTpr;
             const int rows = cur.rows(p);
@@ -255,11 +190,9 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                 }
 #pragma unroll
                 for (int o2 = kTpr / 2; o2 > 0; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
-                // the exponent field of a normal amax; 0 and subnormals as 2^-126
-                const int e = max(1, static_cast<int>(__float_as_uint(amax) >> 23)) - 127;
-                const int up = e == 128 ? 0 : min(126, 14 - e);
-                const float f = __int_as_float((127 + up) << 23);
-                if (part == 0) s_inv[r] = __int_as_float((127 - up) << 23);
+                const int up = row_power(amax);
+                const float f = power_of_two(up);
+                if (part == 0) s_inv[r] = power_of_two(-up);
 #pragma unroll
                 for (int i = 0; i < kCpt; ++i) {
                     const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -345,7 +278,9 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t x = b[2 * kk + h];
-                            mma16816<true>(s[2 * np + h], a, f16x2_of_e4m3(x & 0xFFFFu), f16x2_of_e4m3(x >> 16));
+                            uint32_t b0, b1;
+                            f16x4_of_e4m3(x, b0, b1);
+                            mma16816<true>(s[2 * np + h], a, b0, b1);
                         }
                     }
                 }
@@ -421,8 +356,11 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x = __byte_perm(b[2 * h], 0, 0x3120), y = __byte_perm(b[2 * h + 1], 0, 0x3120);
                         const int ch = 2 * dp + h;
-                        mma16816<true>(o[2 * ch], ph, f16x2_of_e4m3(x & 0xFFFFu), f16x2_of_e4m3(y & 0xFFFFu));
-                        mma16816<true>(o[2 * ch + 1], ph, f16x2_of_e4m3(x >> 16), f16x2_of_e4m3(y >> 16));
+                        uint32_t x0, x1, y0, y1;
+                        f16x4_of_e4m3(x, x0, x1);
+                        f16x4_of_e4m3(y, y0, y1);
+                        mma16816<true>(o[2 * ch], ph, x0, y0);
+                        mma16816<true>(o[2 * ch + 1], ph, x1, y1);
                     }
                 }
             }
@@ -728,8 +666,14 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
     p.min_blocks = 1;
     p.wait_at_end = 0;
     p.tile_rows = kFewRows;
-    int r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
-    if (r != MOE_OK) return r;
+    int r;
+    if (attn_decode_takes(s)) {
+        few = AttnParts{p.part, p.desc, attn_tc_ctas(), kFewRows};
+        if (few.ctas == 0 || launch_attn_decode(p, kD, e4m3, few.ctas, st) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
+        if (r != MOE_OK) return r;
+    }
     launches += 1;
     if (!only_few(s)) {
         p.desc = reinterpret_cast<AttnDesc *>(ws + w.many_desc);

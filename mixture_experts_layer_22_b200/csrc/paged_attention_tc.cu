@@ -36,7 +36,6 @@
 #include <cuda_bf16.h>
 
 #include "paged_work.cuh"
-#include "ptx.cuh"
 
 namespace moe {
 
@@ -65,26 +64,6 @@ __device__ __forceinline__ bool elect_one()
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
     return r != 0;
-}
-
-// Bounded wait for the phase of the given parity, as mbar_wait, but the wall
-// clock is read only every 256 tries: a wait here is on the critical path of
-// every block, and reading the clock takes longer than the phase.
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
-{
-    uint64_t t0 = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 255u) == 0) {
-            if (*abort_flag) return false;
-            const uint64_t now = globaltimer();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kTimeoutNs) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
 }
 
 // Shared-memory descriptor of an operand stored with its M or N dimension
@@ -230,7 +209,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
     const uint32_t tmem = s_tmem;
     // a wait's answer is the whole warp's
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, tc_wait(smem_u32(bar), parity, &s_abort));
+        return __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, &s_abort));
     };
     const int tile = p.tile_rows >> 1;                       // rows of a tile, at most 128
     long long left = n_blocks;
@@ -603,26 +582,28 @@ static AttnEncodeFn attn_encode_fn()
     return fn;
 }
 
-static bool encode_bf16(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                        const cuuint32_t *box)
+static bool encode(CUtensorMap *m, const void *base, bool codes, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box)
 {
     AttnEncodeFn fn = attn_encode_fn();
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, one,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const bool narrow = box[0] * (codes ? 1 : 2) == 64;
+    return fn && fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+                    const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A cache as [num_pages][page_size][n_kv][D] with boxes of box_rows tokens of one
-// head and 64 columns.
-static bool cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, int box_rows)
+// head and 128 bytes (64 where a row has no more).
+bool attn_cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, bool codes, int box_rows)
 {
+    const cuuint64_t esz = codes ? 1 : 2, row = kD * esz;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_kv), static_cast<cuuint64_t>(p.page_size),
                                 static_cast<cuuint64_t>(p.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(kD) * 2 * p.n_kv,
-                                   static_cast<cuuint64_t>(p.page_stride) * 2};
-    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
-    return encode_bf16(m, base, 4, dims, strides, box);
+    const cuuint64_t strides[3] = {row, row * p.n_kv, static_cast<cuuint64_t>(p.page_stride) * esz};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>((row < 128 ? row : 128) / esz), 1, static_cast<cuuint32_t>(box_rows), 1};
+    return encode(m, base, codes, 4, dims, strides, box);
 }
 
 // Queries as [T][n_heads][D] with boxes of a tile's tokens, one group's heads and
@@ -632,7 +613,7 @@ static bool query_map(CUtensorMap *m, const AttnParams &p, int kD)
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_heads), static_cast<cuuint64_t>(p.T)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
-    return encode_bf16(m, p.q, 3, dims, strides, box);
+    return encode(m, p.q, false, 3, dims, strides, box);
 }
 
 bool attn_tc_takes(const moe_attn_shape_t &s)
@@ -676,8 +657,8 @@ cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool cha
 {
     const int box_rows = p.page_size < 128 ? p.page_size : 128;
     CUtensorMap q, k, v;
-    if (!query_map(&q, p, head_dim) || !cache_map(&k, p.k_cache, p, head_dim, box_rows) ||
-        !cache_map(&v, p.v_cache, p, head_dim, box_rows))
+    if (!query_map(&q, p, head_dim) || !attn_cache_map(&k, p.k_cache, p, head_dim, false, box_rows) ||
+        !attn_cache_map(&v, p.v_cache, p, head_dim, false, box_rows))
         return cudaErrorInvalidValue;
     if (head_dim == 64)
         return launch_kernel(paged_attention_tc_kernel<64>, dim3(ctas), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, q, k, v,

@@ -15,6 +15,7 @@
 // The division depends on lengths and G alone, so results are reproducible.
 #pragma once
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -28,6 +29,26 @@ struct AttnDesc {
     int32_t parts;        // 0: none
     int32_t qs, kvh, row0, rows;
 };
+
+// Bounded wait for the phase of the given parity, as mbar_wait, but the wall
+// clock is read only every 256 tries: a wait here is on the critical path of
+// every block, and reading the clock takes longer than the phase.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kTimeoutNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
 
 struct AttnParams {
     const void *q, *k_cache, *v_cache;
@@ -309,5 +330,11 @@ bool attn_tc_takes(const moe_attn_shape_t &s);
 int attn_tc_rows(const moe_attn_shape_t &s);
 int attn_tc_ctas();
 cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st);
+
+// The decode kernel, one CTA per SM as well.
+bool attn_decode_takes(const moe_attn_shape_t &s);
+cudaError_t launch_attn_decode(const AttnParams &p, int head_dim, bool e4m3, int ctas, cudaStream_t st);
+
+bool attn_cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, bool codes, int box_rows);
 
 }  // namespace moe
