@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 
     Split<128, kRows, kBlk> split;
     Cursor<kRows, kBlk> cur;                     // the compute side
-    const long long n_blocks = split.init(p, cur);
+    const long long n_blocks = split.init(p, cur, reinterpret_cast<long long *>(smem));
     if (n_blocks == 0) {
         if (tid == 0) p.desc[blockIdx.x].parts = 0;
         grid_dep_launch();
@@ -503,90 +503,142 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 struct AttnParts {
     const float *part;
     const AttnDesc *desc;
-    int ctas, rows;
+    int units, rows;          // ranges, and query rows of an item
 };
 
-// Joins the parts of the items that lie in several CTAs' ranges, of one or two
-// kernels.  A block has one item (by the CTA that started it) and 32 of its rows,
-// 16 for the first kernel: a warp takes kR rows side by side, kD / 32 elements a
-// lane.  The parts' maxima and totals are read by a lane each.
-template <int kD, int kR>
-__device__ __forceinline__ void combine_rows(const AttnParams &p, const AttnParts &from, int c, int row)
+// One row of an item in several ranges: its sums over parts first .. behind - 1,
+// relative to the largest maximum of all its parts, kD / 32 elements a lane; l is
+// the total over those parts, in every lane.
+template <int kD>
+__device__ __forceinline__ void join_row(const AttnParts &from, int c, int parts, int r, int first, int behind, float (&acc)[kD / 32], float &l)
 {
     constexpr int kE = kD / 32;
     const int lane = threadIdx.x & 31;
-    const AttnDesc d = from.desc[c];
-    if (d.parts < 2 || row >= d.rows) return;
     const long long stride = static_cast<long long>(from.rows) * (kD + 2);
     // part k of the item
     auto part = [&](int k) { return from.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
-    float base[kR], l[kR], acc[kR][kE];
-#pragma unroll
-    for (int j = 0; j < kR; ++j) {
-        base[j] = -INFINITY;
-        for (int k = lane; k < d.parts; k += 32) base[j] = fmaxf(base[j], row + j < d.rows ? part(k)[from.rows * kD + row + j] : -INFINITY);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) base[j] = fmaxf(base[j], __shfl_xor_sync(0xffffffffu, base[j], o));
-        if (base[j] == -INFINITY) base[j] = 0.0f;
-        l[j] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) acc[j][e] = 0.0f;
-    }
-    for (int k0 = 0; k0 < d.parts; k0 += 32) {
-        float f[kR];
-#pragma unroll
-        for (int j = 0; j < kR; ++j) {
-            f[j] = 0.0f;
-            if (k0 + lane < d.parts && row + j < d.rows) {
-                const float *q = part(k0 + lane) + from.rows * kD + row + j;
-                f[j] = exp2_fast(q[0] - base[j]);
-                l[j] += f[j] * q[from.rows];
-            }
-        }
-        const int n = min(32, d.parts - k0);
+    const int at_m = from.rows * kD + r, at_l = at_m + from.rows;
+    float base = -INFINITY;
 #pragma unroll 4
+    for (int k = lane; k < parts; k += 32) base = fmaxf(base, part(k)[at_m]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) base = fmaxf(base, __shfl_xor_sync(0xffffffffu, base, o));
+    if (base == -INFINITY) base = 0.0f;
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+    for (int k0 = first; k0 < behind; k0 += 32) {
+        float f = 0.0f;
+        if (k0 + lane < behind) {
+            const float *q = part(k0 + lane);
+            f = exp2_fast(q[at_m] - base);
+            l += f * q[at_l];
+        }
+        const int n = min(32, behind - k0);
+#pragma unroll 8
         for (int k = 0; k < n; ++k) {
-            const float *q = part(k0 + k) + static_cast<long long>(row) * kD + lane * kE;
+            const float *q = part(k0 + k) + r * kD + lane * kE;
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            float v[kE];
+            if constexpr (kE == 2) {
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kR; ++j) {
-                const float fk = __shfl_sync(0xffffffffu, f[j], k);
-                if (row + j >= d.rows) continue;             // the same for the whole warp
-                float v[kE];
-                if constexpr (kE == 2) {
-                    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q + j * kD);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kE; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + j * kD + e);
-                }
-#pragma unroll
-                for (int e = 0; e < kE; ++e) acc[j][e] += fk * v[e];
+                for (int e = 0; e < kE; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(q + e);
             }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) acc[e] += fk * v[e];
         }
     }
 #pragma unroll
-    for (int j = 0; j < kR; ++j) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
-        if (row + j >= d.rows) break;
-        const float inv = l[j] > 0.0f ? p.v_scale / l[j] : l[j] == 0.0f ? 0.0f : l[j];
-        const int grow = d.row0 + row + j;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                             (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
-                             lane * kE;
-#pragma unroll
-        for (int e = 0; e < kE; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[j][e] * inv, acc[j][e + 1] * inv);
-    }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 }
+
+template <int kD>
+__device__ __forceinline__ void put_row(const AttnParams &p, const AttnDesc &d, int r, const float (&acc)[kD / 32], float l)
+{
+    constexpr int kE = kD / 32;
+    const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
+    const int grow = d.row0 + r;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                         (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
+                         (threadIdx.x & 31) * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// Joins the parts of the items that lie in several ranges, of one or two kernels.
+// First kernel (items of up to 16 rows, up to 8 ranges per SM): a block has 8
+// ranges and every fourth row of the items that they start; a warp joins its
+// item's row alone, and where an item has many parts (few requests, long
+// sequences) the 8 warps share them.  Second kernel (items of many rows): a block
+// has one range and 32 rows of its item, a warp a row.
+constexpr int kManyParts = 16;
 
 template <int kD>
 __global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams p, const AttnParts few, const AttnParts many)
 {
-    const int warp = threadIdx.x >> 5, per = (many.rows + 31) / 32;
+    constexpr int kE = kD / 32;
+    __shared__ float s_acc[8][kD], s_l[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int few_blocks = (few.units + 7) / 8 * 4;
+    float acc[kE], l;
     grid_dep_wait();
-    const int x = static_cast<int>(blockIdx.x) - few.ctas;
-    if (x < 0) combine_rows<kD, 2>(p, few, blockIdx.x, 2 * warp);
-    else combine_rows<kD, 4>(p, many, x / per, x % per * 32 + 4 * warp);
+    if (static_cast<int>(blockIdx.x) >= few_blocks) {
+        const int per = (many.rows + 31) / 32, x = blockIdx.x - few_blocks, c = x / per;
+        const AttnDesc d = many.desc[c];
+        if (d.parts < 2) return;
+        for (int r = x % per * 32 + warp; r < min(d.rows, x % per * 32 + 32); r += 8) {
+            join_row<kD>(many, c, d.parts, r, 0, d.parts, acc, l);
+            put_row<kD>(p, d, r, acc, l);
+        }
+        return;
+    }
+    const int c0 = blockIdx.x / 4 * 8, y = blockIdx.x % 4;
+    const int parts = lane < 8 && c0 + lane < few.units ? few.desc[c0 + lane].parts : 0;      // the same in every warp
+    const int own = __shfl_sync(0xffffffffu, parts, warp);
+    if (own >= 2 && own <= kManyParts) {
+        const AttnDesc d = few.desc[c0 + warp];
+        for (int r = y; r < d.rows; r += 4) {
+            join_row<kD>(few, c0 + warp, own, r, 0, own, acc, l);
+            put_row<kD>(p, d, r, acc, l);
+        }
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, parts > kManyParts); left; left &= left - 1) {
+        const int i = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, parts, i);
+        const AttnDesc d = few.desc[c0 + i];
+        for (int r = y; r < d.rows; r += 4) {
+            join_row<kD>(few, c0 + i, n, r, n * warp / 8, n * (warp + 1) / 8, acc, l);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) s_acc[warp][lane * kE + e] = acc[e];
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < 8; ++w) {
+                    l += s_l[w];
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) acc[e] += s_acc[w][lane * kE + e];
+                }
+                put_row<kD>(p, d, r, acc, l);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// SMs of the current device (0 on an error), up to what the workspace holds.
+static int sm_count()
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int n = dev >= 0 && dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (n > kAttnMaxSms) n = kAttnMaxSms;
+        if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 // CTAs of a kernel that are resident on the GPU at once, found once per kernel
@@ -606,7 +658,7 @@ static int resident_ctas()
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, 128, C::kSmem) != cudaSuccess || per < 1) return 0;
         n = sms * per;
-        if (n > kAttnMaxCtas) n = kAttnMaxCtas;
+        if (n > kAttnMaxUnits) n = kAttnMaxUnits;
         if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
     }
     return n;
@@ -617,8 +669,8 @@ static int launch_mma(const AttnParams &p, AttnParts &parts, bool chained, cudaS
 {
     using C = AttnCfg<kD, kE4m3, kWM>;
     parts = AttnParts{p.part, p.desc, resident_ctas<kD, kE4m3, kWM>(), C::kRows};
-    if (parts.ctas == 0) return MOE_ERR_CUDA;
-    return launch_kernel(paged_attention_kernel<kD, kE4m3, kWM>, dim3(parts.ctas), dim3(128), C::kSmem, st, chained, p) == cudaSuccess
+    if (parts.units == 0) return MOE_ERR_CUDA;
+    return launch_kernel(paged_attention_kernel<kD, kE4m3, kWM>, dim3(parts.units), dim3(128), C::kSmem, st, chained, p) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -642,14 +694,14 @@ struct AttnWs {
 static AttnWs attn_ws(const moe_attn_shape_t &s)
 {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    auto parts = [&](int ctas, int rows) { return up(static_cast<size_t>(ctas) * 2 * rows * (s.head_dim + 2) * 4); };
+    auto parts = [&](int units, int rows) { return up(static_cast<size_t>(units) * 2 * rows * (s.head_dim + 2) * 4); };
     AttnWs w;
     w.few_desc = 0;
-    w.many_desc = up(sizeof(AttnDesc) * kAttnMaxCtas);
+    w.many_desc = up(sizeof(AttnDesc) * kAttnMaxUnits);
     w.few_part = 2 * w.many_desc;
-    w.many_part = w.few_part + parts(kAttnMaxCtas, kFewRows);
+    w.many_part = w.few_part + parts(kAttnMaxUnits, kFewRows);
     w.total = w.many_part;
-    if (!only_few(s)) w.total += attn_tc_takes(s) ? parts(kAttnTcMaxCtas, attn_tc_rows(s)) : parts(kAttnMaxCtas, 64);
+    if (!only_few(s)) w.total += attn_tc_takes(s) ? parts(kAttnMaxSms, attn_tc_rows(s)) : parts(kAttnMaxUnits, 64);
     return w;
 }
 
@@ -659,17 +711,18 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
     const AttnWs w = attn_ws(s);
     const bool e4m3 = s.cache_dtype == MOE_E4M3;
     AttnParts few, many = {nullptr, nullptr, 0, 0};
+    const int sms = sm_count();
+    if (sms == 0) return MOE_ERR_CUDA;
     p.desc = reinterpret_cast<AttnDesc *>(ws + w.few_desc);
     p.part = reinterpret_cast<float *>(ws + w.few_part);
     p.min_rows = 1;
     p.max_rows = only_few(s) ? 0x7fffffff : kFewRows;
-    p.min_blocks = 1;
     p.wait_at_end = 0;
     p.tile_rows = kFewRows;
     int r;
     if (attn_decode_takes(s)) {
-        few = AttnParts{p.part, p.desc, attn_tc_ctas(), kFewRows};
-        if (few.ctas == 0 || launch_attn_decode(p, kD, e4m3, few.ctas, st) != cudaSuccess) return MOE_ERR_CUDA;
+        few = AttnParts{p.part, p.desc, sms * kDecodeWarps, kFewRows};
+        if (launch_attn_decode(p, kD, e4m3, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
     } else {
         r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
         if (r != MOE_OK) return r;
@@ -683,8 +736,8 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         p.wait_at_end = 1;
         if (attn_tc_takes(s)) {
             p.tile_rows = attn_tc_rows(s);
-            many = AttnParts{p.part, p.desc, attn_tc_ctas(), p.tile_rows};
-            if (many.ctas == 0 || launch_attn_tc(p, kD, many.ctas, true, st) != cudaSuccess) return MOE_ERR_CUDA;
+            many = AttnParts{p.part, p.desc, sms, p.tile_rows};
+            if (launch_attn_tc(p, kD, sms, true, st) != cudaSuccess) return MOE_ERR_CUDA;
         } else {
             p.tile_rows = 64;
             r = e4m3 ? launch_mma<kD, true, 4>(p, many, true, st) : launch_mma<kD, false, 4>(p, many, true, st);
@@ -692,7 +745,7 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         }
         launches += 1;
     }
-    if (launch_kernel(attention_combine_kernel<kD>, dim3(few.ctas + many.ctas * ((many.rows + 31) / 32)), dim3(256), 0, st, true, p, few, many) !=
+    if (launch_kernel(attention_combine_kernel<kD>, dim3((few.units + 7) / 8 * 4 + many.units * ((many.rows + 31) / 32)), dim3(256), 0, st, true, p, few, many) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
     launches += 1;

@@ -30,7 +30,6 @@
 // blocks share one ring of slots in the order K0 V0 K1 V1 ...; a block is put
 // together from one TMA box per page and 64 columns, whose page ids the 32 lanes
 // of the load warp read side by side.
-#include <atomic>
 #include <mutex>
 
 #include <cuda_bf16.h>
@@ -197,8 +196,10 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
     tc_fence_before();
     Split<C::kThreads, 0, kBlk> split;
     Cursor<0, kBlk> cur;
-    const long long n_blocks = split.init(p, cur);           // has block barriers
+    const long long n_blocks = split.init(p, cur, reinterpret_cast<long long *>(smem));           // has block barriers
     tc_fence_after();
+    fence_async_smem();                                      // its shared memory is TMA's now
+    __syncthreads();
     grid_dep_launch();
     if (n_blocks == 0) {
         if (tid == 0) p.desc[blockIdx.x].parts = 0;
@@ -582,28 +583,26 @@ static AttnEncodeFn attn_encode_fn()
     return fn;
 }
 
-static bool encode(CUtensorMap *m, const void *base, bool codes, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+static bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box)
 {
     AttnEncodeFn fn = attn_encode_fn();
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    const bool narrow = box[0] * (codes ? 1 : 2) == 64;
-    return fn && fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
-                    const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A cache as [num_pages][page_size][n_kv][D] with boxes of box_rows tokens of one
-// head and 128 bytes (64 where a row has no more).
-bool attn_cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, bool codes, int box_rows)
+// head and 64 columns.
+static bool cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, int box_rows)
 {
-    const cuuint64_t esz = codes ? 1 : 2, row = kD * esz;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_kv), static_cast<cuuint64_t>(p.page_size),
                                 static_cast<cuuint64_t>(p.num_pages)};
-    const cuuint64_t strides[3] = {row, row * p.n_kv, static_cast<cuuint64_t>(p.page_stride) * esz};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>((row < 128 ? row : 128) / esz), 1, static_cast<cuuint32_t>(box_rows), 1};
-    return encode(m, base, codes, 4, dims, strides, box);
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(kD) * 2 * p.n_kv,
+                                   static_cast<cuuint64_t>(p.page_stride) * 2};
+    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+    return encode(m, base, 4, dims, strides, box);
 }
 
 // Queries as [T][n_heads][D] with boxes of a tile's tokens, one group's heads and
@@ -613,7 +612,7 @@ static bool query_map(CUtensorMap *m, const AttnParams &p, int kD)
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(p.n_heads), static_cast<cuuint64_t>(p.T)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
-    return encode(m, p.q, false, 3, dims, strides, box);
+    return encode(m, p.q, 3, dims, strides, box);
 }
 
 bool attn_tc_takes(const moe_attn_shape_t &s)
@@ -634,36 +633,22 @@ int attn_tc_rows(const moe_attn_shape_t &s)
     return 2 * group * (128 / group);
 }
 
-int attn_tc_ctas()
+cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int sms, bool chained, cudaStream_t st)
 {
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    int n = dev >= 0 && dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        if (cudaFuncSetAttribute(paged_attention_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<64>::kSmem) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(paged_attention_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<128>::kSmem) !=
-                cudaSuccess)
-            return 0;
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n > kAttnTcMaxCtas) n = kAttnTcMaxCtas;
-        if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
-cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st)
-{
+    static PerDeviceOnce once;
+    once([] {
+        cudaFuncSetAttribute(paged_attention_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<64>::kSmem);
+        cudaFuncSetAttribute(paged_attention_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<128>::kSmem);
+    });
     const int box_rows = p.page_size < 128 ? p.page_size : 128;
     CUtensorMap q, k, v;
-    if (!query_map(&q, p, head_dim) || !attn_cache_map(&k, p.k_cache, p, head_dim, false, box_rows) ||
-        !attn_cache_map(&v, p.v_cache, p, head_dim, false, box_rows))
+    if (!query_map(&q, p, head_dim) || !cache_map(&k, p.k_cache, p, head_dim, box_rows) ||
+        !cache_map(&v, p.v_cache, p, head_dim, box_rows))
         return cudaErrorInvalidValue;
     if (head_dim == 64)
-        return launch_kernel(paged_attention_tc_kernel<64>, dim3(ctas), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, q, k, v,
+        return launch_kernel(paged_attention_tc_kernel<64>, dim3(sms), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, q, k, v,
                              p, box_rows);
-    return launch_kernel(paged_attention_tc_kernel<128>, dim3(ctas), dim3(TcCfg<128>::kThreads), TcCfg<128>::kSmem, st, chained, q, k, v, p,
+    return launch_kernel(paged_attention_tc_kernel<128>, dim3(sms), dim3(TcCfg<128>::kThreads), TcCfg<128>::kSmem, st, chained, q, k, v, p,
                          box_rows);
 }
 

@@ -4,15 +4,16 @@
 // a request is token r / group, query head kv_head * group + r % group, so that
 // the heads that share a key/value head share its loads.  An item has as many
 // blocks of keys as its last row sees.  The blocks of all items, in the order
-// request, key/value head, tile, block, are numbered through, and CTA c of G
-// takes the numbers [W c / G, W (c + 1) / G).  Every CTA thus has the same work
-// however ragged the lengths are, a long sequence is split over many CTAs and
-// neighbours read the same keys at the same time.  An item that lies whole in
-// one CTA's range is written by it; of an item over several CTAs each writes a
-// partial result (unnormalised sums, their maximum and total), and a second
-// kernel joins them in CTA order.  A CTA has at most two partial items: the one
-// it continues (slot 0) and the one it starts and does not finish (slot 1).
-// The division depends on lengths and G alone, so results are reproducible.
+// request, key/value head, tile, block, are numbered through and cut into G equal
+// ranges, range c being the numbers [W c / G, W (c + 1) / G): one for each CTA, or
+// for each warp.  All thus have the same work however ragged the lengths are, a
+// long sequence is split over many and neighbours read the same keys at the same
+// time.  An item that lies whole in one range is written by its owner; of an item
+// over several ranges each owner writes a partial result (unnormalised sums, their
+// maximum and total), and a second kernel joins them in order.  A range has at
+// most two partial items: the one it continues (slot 0) and the one it starts and
+// does not finish (slot 1).  The division depends on lengths and G alone, so
+// results are reproducible.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -20,10 +21,10 @@
 namespace moe {
 
 constexpr int kAttnMaxB = 4096;
-constexpr int kAttnMaxCtas = 160 * 4;       // resident CTAs of one kernel, at most
-constexpr int kAttnTcMaxCtas = 160;         // the tensor-memory kernel has one per SM
+constexpr int kAttnMaxSms = 160;
+constexpr int kAttnMaxUnits = kAttnMaxSms * 8;   // ranges of one kernel: up to 8 warps or 4 CTAs per SM
 
-// What a combine block needs to know of the item that CTA c started and did not
+// What a combine block needs to know of the item that range c starts and does not
 // finish: its parts are (c, slot 1), (c + 1, slot 0), ... (c + parts - 1, slot 0).
 struct AttnDesc {
     int32_t parts;        // 0: none
@@ -61,7 +62,6 @@ struct AttnParams {
     int B, T, n_heads, n_kv, group, page_size, num_pages, max_pages, causal;
     int min_rows, max_rows;   // this kernel's requests: rows in [min_rows, max_rows]
     int tile_rows;            // query rows of an item
-    int min_blocks;           // a CTA gets at least this many blocks
     int wait_at_end;          // launched while the kernel before it runs
     float scale_log2, v_scale;
 };
@@ -212,20 +212,23 @@ struct Cursor {
     }
 };
 
-// The division itself.  init() finds where CTA blockIdx.x starts (cur) and
-// returns how many blocks it has; block-collective over kThreads threads, every
-// thread gets the same answer.
-template <int kThreads, int kRows, int kBlk>
+// The division itself.  A CTA has kUnits ranges, one for each of its first kUnits
+// warps (range warp * gridDim.x + blockIdx.x, so that few ranges spread over all
+// SMs), or one for all.  init() finds where the calling thread's range starts (cur)
+// and returns how many blocks it has; block-collective over kThreads threads, with
+// kThreads words of shared memory to itself meanwhile.
+template <int kThreads, int kRows, int kBlk, int kUnits = 1>
 struct Split {
     long long W;          // blocks in all
-    int G;                // CTAs that share them
+    int G;                // ranges that share them
 
-    __device__ __forceinline__ long long cta_start(int c) const { return div_ll(W * c, G); }
+    __device__ __forceinline__ long long start(int c) const { return div_ll(W * c, G); }
+    static __device__ __forceinline__ int unit(int k) { return k * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); }
 
-    __device__ __forceinline__ long long init(const AttnParams &p, Cursor<kRows, kBlk> &cur)
+    __device__ __forceinline__ long long init(const AttnParams &p, Cursor<kRows, kBlk> &cur, long long *s_before)
     {
         __shared__ long long s_warp[kThreads / 32];
-        __shared__ int s_at[4];
+        __shared__ int s_at[kUnits][4];
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int chunk = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
@@ -248,15 +251,22 @@ struct Split {
             if (w < warp) before += s_warp[w];
             W += s_warp[w];
         }
-        const long long most = div_ll(W + p.min_blocks - 1, p.min_blocks);
-        G = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-        const int c = blockIdx.x;
-        if (c >= G) return 0;
-        const long long w0 = cta_start(c), n = cta_start(c + 1) - w0;
-        if (n > 0 && w0 >= before && w0 < before + sum) {
-            // the start lies in this thread's requests
-            long long at = w0 - before;
-            int b = b0;
+        s_before[tid] = before;
+        const int units = static_cast<int>(gridDim.x) * kUnits;
+        G = W < units ? static_cast<int>(W) : units;
+        if (unit(0) >= G) return 0;                          // none of the CTA's ranges
+        __syncthreads();
+        if (tid < kUnits && unit(tid) < G) {
+            long long at = start(unit(tid));
+            // the thread in whose requests it lies: the last one with before <= at
+            int lo = 0, hi = kThreads;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_before[mid] <= at) lo = mid;
+                else hi = mid;
+            }
+            at -= s_before[lo];
+            int b = min(p.B, lo * chunk);
             Req r;
             long long per_head;
             for (;; ++b) {
@@ -273,68 +283,61 @@ struct Split {
                 const int nb = tile_blocks<kBlk>(p, r, rows - 1);
                 tile = static_cast<int>(div_ll(at, nb));
                 at -= static_cast<long long>(tile) * nb;
+            } else if (per % p.group == 0 && r.kv >= r.n) {
+                const int step = per / p.group;
+                const long long base = r.kv - r.n + step + kBlk - 1;
+                int first = 0, behind = tiles;               // blocks before `first` <= at < blocks before `behind`
+                while (behind - first > 1) {
+                    const int mid = (first + behind) >> 1;
+                    if (floor_sum(mid, kBlk, step, base) <= at) first = mid;
+                    else behind = mid;
+                }
+                tile = first;
+                if (first > 0) at -= floor_sum(first, kBlk, step, base);
             } else {
-                // the blocks before tile i, by a request cut to its first i
-                // tiles' tokens, or tile by tile
-                if (per % p.group == 0 && r.kv >= r.n) {
-                    const int step = per / p.group;
-                    const long long base = r.kv - r.n + step + kBlk - 1;
-                    int lo = 0, hi = tiles;           // before(lo) <= at < before(hi)
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (floor_sum(mid, kBlk, step, base) <= at) lo = mid;
-                        else hi = mid;
-                    }
-                    tile = lo;
-                    if (lo > 0) at -= floor_sum(lo, kBlk, step, base);
-                } else {
-                    for (;; ++tile) {
-                        const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * per, rows) - 1);
-                        if (at < nb) break;
-                        at -= nb;
-                    }
+                for (;; ++tile) {
+                    const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * per, rows) - 1);
+                    if (at < nb) break;
+                    at -= nb;
                 }
             }
-            s_at[0] = b;
-            s_at[1] = kvh;
-            s_at[2] = tile;
-            s_at[3] = static_cast<int>(at);
+            s_at[tid][0] = b;
+            s_at[tid][1] = kvh;
+            s_at[tid][2] = tile;
+            s_at[tid][3] = static_cast<int>(at);
         }
         __syncthreads();
-        if (n > 0) {
-            cur.b = s_at[0];
-            cur.kvh = s_at[1];
-            cur.tile = s_at[2];
-            cur.blk = s_at[3];
-            cur.r = attn_request(p, cur.b, bad);
-            cur.enter_request(p);
-            cur.enter(p);
-        }
-        return n;
+        const int k = kUnits > 1 ? warp : 0;
+        if (k >= kUnits || unit(k) >= G) return 0;
+        cur.b = s_at[k][0];
+        cur.kvh = s_at[k][1];
+        cur.tile = s_at[k][2];
+        cur.blk = s_at[k][3];
+        cur.r = attn_request(p, cur.b, bad);
+        cur.enter_request(p);
+        cur.enter(p);
+        return start(unit(k) + 1) - start(unit(k));
     }
 
-    // CTAs over which the item extends that CTA c starts at `from_start` blocks
-    // into its range and that has `blocks` blocks.
+    // Ranges over which the item extends that range c starts at `from_start`
+    // blocks into it and that has `blocks` blocks.
     __device__ __forceinline__ int parts(int c, long long from_start, int blocks) const
     {
-        const long long end = cta_start(c) + from_start + blocks;
-        int k = 1;
-        while (cta_start(c + k) < end) ++k;
-        return k;
+        // the first range x with W x / G >= its end is the first one behind it
+        const long long end = start(c) + from_start + blocks;
+        return static_cast<int>(div_ll(end * G + W - 1, W)) - c;
     }
 };
 
 // The tensor-memory kernel: whether it takes a shape, the query rows of its items,
-// its CTAs on this device (0 on an error), its launch.
+// its launch with one CTA (and range) per SM.
 bool attn_tc_takes(const moe_attn_shape_t &s);
 int attn_tc_rows(const moe_attn_shape_t &s);
-int attn_tc_ctas();
-cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int ctas, bool chained, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int sms, bool chained, cudaStream_t st);
 
-// The decode kernel, one CTA per SM as well.
+// The decode kernel, one CTA of kDecodeWarps ranges per SM.
+constexpr int kDecodeWarps = 8;
 bool attn_decode_takes(const moe_attn_shape_t &s);
-cudaError_t launch_attn_decode(const AttnParams &p, int head_dim, bool e4m3, int ctas, cudaStream_t st);
-
-bool attn_cache_map(CUtensorMap *m, const void *base, const AttnParams &p, int kD, bool codes, int box_rows);
+cudaError_t launch_attn_decode(const AttnParams &p, int head_dim, bool e4m3, int sms, cudaStream_t st);
 
 }  // namespace moe
