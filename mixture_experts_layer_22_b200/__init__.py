@@ -253,81 +253,83 @@ def inv_rope_quant(shape, x, positions, cos_sin, q, scales, status=None, stream=
            "moe_inv_rope_quant_per_head")
 
 
-def _dense(t, dtype, shape, what):
+# The calls below launch on the current device, `dev` in these checks: every
+# tensor has to be there (get_device() is -1 for a host tensor).
+
+def _dense(t, dtype, shape, dev, what):
     """Device address of a dense tensor of exactly this type and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: dense device tensor {shape} {dtype} expected, got {tuple(t.shape)} {t.dtype} strides "
-                         f"{t.stride()} on {t.device}")
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: dense {dtype} tensor {shape} on cuda:{dev} expected, got {t.dtype} {tuple(t.shape)} "
+                         f"strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, n, heads, dim, stride, what):
-    """Device address of [n, heads, dim] bf16 rows `stride` elements apart (0: adjacent)."""
+def _rows(t, shape, stride, dev, what):
+    """Device address of bf16 rows [n, heads, dim], `stride` elements apart (0: adjacent)."""
+    n, heads, dim = shape
+    step = stride or heads * dim
     at = t.stride()
-    if (t.dtype != torch.bfloat16 or t.shape != (n, heads, dim) or not t.is_cuda or at[2] != 1 or
-            (heads > 1 and at[1] != dim) or (n > 1 and at[0] != (stride or heads * dim))):
-        raise ValueError(f"{what}: bf16 device tensor {(n, heads, dim)} with rows {stride or heads * dim} elements "
-                         f"apart expected, got {tuple(t.shape)} {t.dtype} strides {at} on {t.device}")
-    return t.data_ptr()
-
-
-def _cache(t, s, what):
-    """Device address of a cache [num_pages, page_size, n_kv_heads, head_dim]."""
-    row = s.n_kv_heads * s.head_dim
-    page = s.page_stride or s.page_size * row
-    at = t.stride()
-    if (t.dtype not in _CACHE_DTYPES[s.cache_dtype] or not t.is_cuda or
-            t.shape != (s.num_pages, s.page_size, s.n_kv_heads, s.head_dim) or at[3] != 1 or
-            (s.n_kv_heads > 1 and at[2] != s.head_dim) or (s.page_size > 1 and at[1] != row) or
-            (s.num_pages > 1 and at[0] != page)):
-        raise ValueError(f"{what}: device cache {(s.num_pages, s.page_size, s.n_kv_heads, s.head_dim)} with pages {page} "
-                         f"elements apart expected, got {tuple(t.shape)} {t.dtype} strides {at} on {t.device}")
+    if (t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != shape or
+            at != (step, dim, 1) and (at[2] != 1 or heads > 1 and at[1] != dim or n > 1 and at[0] != step)):
+        raise ValueError(f"{what}: bf16 tensor {shape} with rows {step} elements apart on cuda:{dev} expected, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {at} on {t.device}")
     return t.data_ptr()
 
 
 _CACHE_DTYPES = {BF16: (torch.bfloat16,), E4M3: (torch.uint8, torch.float8_e4m3fn)}
+
+
+def _caches(k, v, s, dev):
+    """Device addresses of a K and a V cache [num_pages, page_size, n_kv_heads, head_dim]."""
+    shape = n, ps, heads, dim = s.num_pages, s.page_size, s.n_kv_heads, s.head_dim
+    row = heads * dim
+    step = s.page_stride or ps * row
+    dtypes = _CACHE_DTYPES.get(s.cache_dtype, ())
+    for t, what in ((k, "k_cache"), (v, "v_cache")):
+        at = t.stride()
+        if (t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or
+                at != (step, row, dim, 1) and (at[3] != 1 or heads > 1 and at[2] != dim or ps > 1 and at[1] != row or
+                                               n > 1 and at[0] != step)):
+            raise ValueError(f"{what}: cache {shape} of {dtypes} with pages {step} elements apart on cuda:{dev} expected, "
+                             f"got {t.dtype} {tuple(t.shape)} strides {at} on {t.device}")
+    return k.data_ptr(), v.data_ptr()
+
+
 _I32 = torch.int32
 
 
-def _word(t, what):
-    return None if t is None else _dense(t, _I32, (1,), what)
-
-
-def _same_device(*tensors):
-    """The calls launch on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+def _word(t, dev, what):
+    return None if t is None else _dense(t, _I32, (1,), dev, what)
 
 
 def page_plan(shape, cached, fresh, free_pages, block_table, q_start, kv_len, positions, slots, free_next=None,
               free_pos=None, status=None, stream=None):
     """Block table entries, row ranges, positions and cache slots of a batch,
     from its lengths (one launch)."""
-    s = shape
-    _same_device(cached, fresh, free_pages, block_table, q_start, kv_len, positions, slots, free_next, free_pos, status)
+    s, dev = shape, torch.cuda.current_device()
+    B, rows = (s.B,), (s.max_tokens,)
     _check(lib().moe_page_plan(
-        C.byref(s), _dense(cached, _I32, (s.B,), "cached"), _dense(fresh, _I32, (s.B,), "fresh"),
-        _dense(free_pages, _I32, (s.n_free,), "free_pages"), _word(free_pos, "free_pos"),
-        _dense(block_table, _I32, (s.B, s.max_pages), "block_table"), _dense(q_start, _I32, (s.B + 1,), "q_start"),
-        _dense(kv_len, _I32, (s.B,), "kv_len"), _dense(positions, _I32, (s.max_tokens,), "positions"),
-        _dense(slots, _I32, (s.max_tokens,), "slots"), _word(free_next, "free_next"), _word(status, "status"),
-        _stream(stream)), "moe_page_plan")
+        C.byref(s), _dense(cached, _I32, B, dev, "cached"), _dense(fresh, _I32, B, dev, "fresh"),
+        _dense(free_pages, _I32, (s.n_free,), dev, "free_pages"), _word(free_pos, dev, "free_pos"),
+        _dense(block_table, _I32, (s.B, s.max_pages), dev, "block_table"),
+        _dense(q_start, _I32, (s.B + 1,), dev, "q_start"), _dense(kv_len, _I32, B, dev, "kv_len"),
+        _dense(positions, _I32, rows, dev, "positions"), _dense(slots, _I32, rows, dev, "slots"),
+        _word(free_next, dev, "free_next"), _word(status, dev, "status"), _stream(stream)), "moe_page_plan")
 
 
 def rope_append(shape, q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache, status=None, stream=None):
     """Rotary embedding of q and k, and k and v into their cache slots (one launch)."""
-    s = shape
+    s, dev = shape, torch.cuda.current_device()
     n = s.num_tokens
-    _same_device(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache, status)
+    heads, kv_heads = (n, s.n_heads, s.head_dim), (n, s.n_kv_heads, s.head_dim)
     _check(lib().moe_rope_append(
-        C.byref(s), _rows(q, n, s.n_heads, s.head_dim, s.q_stride, "q"),
-        _rows(k, n, s.n_kv_heads, s.head_dim, s.k_stride, "k"), _rows(v, n, s.n_kv_heads, s.head_dim, s.v_stride, "v"),
-        None if positions is None else _dense(positions, _I32, (n,), "positions"), _dense(slots, _I32, (n,), "slots"),
-        None if cos_sin is None else _dense(cos_sin, torch.float32, (s.max_pos, s.rot_dim), "cos_sin"),
-        _rows(q_out, n, s.n_heads, s.head_dim, 0, "q_out"), _cache(k_cache, s, "k_cache"), _cache(v_cache, s, "v_cache"),
-        _word(status, "status"), _stream(stream)), "moe_rope_append")
+        C.byref(s), _rows(q, heads, s.q_stride, dev, "q"), _rows(k, kv_heads, s.k_stride, dev, "k"),
+        _rows(v, kv_heads, s.v_stride, dev, "v"),
+        None if positions is None else _dense(positions, _I32, (n,), dev, "positions"),
+        _dense(slots, _I32, (n,), dev, "slots"),
+        None if cos_sin is None else _dense(cos_sin, torch.float32, (s.max_pos, s.rot_dim), dev, "cos_sin"),
+        _rows(q_out, heads, 0, dev, "q_out"), *_caches(k_cache, v_cache, s, dev), _word(status, dev, "status"),
+        _stream(stream)), "moe_rope_append")
 
 
 def attn_workspace_size(shape: AttnShape) -> int:
@@ -342,14 +344,14 @@ def attn_workspace(shape: AttnShape, device="cuda") -> torch.Tensor:
 
 def paged_attention(shape, q, k_cache, v_cache, block_table, q_start, kv_len, out, ws, status=None, stream=None):
     """Attention of a batch's new tokens over the paged cache that holds them."""
-    s = shape
-    _same_device(q, k_cache, v_cache, block_table, q_start, kv_len, out, ws, status)
+    s, dev = shape, torch.cuda.current_device()
+    rows, ws_bytes = (s.num_tokens, s.n_heads, s.head_dim), ws.numel()
     _check(lib().moe_paged_attention(
-        C.byref(s), _rows(q, s.num_tokens, s.n_heads, s.head_dim, s.q_stride, "q"), _cache(k_cache, s, "k_cache"),
-        _cache(v_cache, s, "v_cache"), _dense(block_table, _I32, (s.B, s.max_pages), "block_table"),
-        _dense(q_start, _I32, (s.B + 1,), "q_start"), _dense(kv_len, _I32, (s.B,), "kv_len"),
-        _rows(out, s.num_tokens, s.n_heads, s.head_dim, 0, "out"), _word(status, "status"), _ptr(ws), ws.numel(),
-        _stream(stream)), "moe_paged_attention")
+        C.byref(s), _rows(q, rows, s.q_stride, dev, "q"), *_caches(k_cache, v_cache, s, dev),
+        _dense(block_table, _I32, (s.B, s.max_pages), dev, "block_table"),
+        _dense(q_start, _I32, (s.B + 1,), dev, "q_start"), _dense(kv_len, _I32, (s.B,), dev, "kv_len"),
+        _rows(out, rows, 0, dev, "out"), _word(status, dev, "status"), _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"),
+        ws_bytes, _stream(stream)), "moe_paged_attention")
 
 
 def selftest_wait_timeout(ws, gave_up, stream=None):
