@@ -737,7 +737,7 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         if (attn_tc_takes(s)) {
             p.tile_rows = attn_tc_rows(s);
             many = AttnParts{p.part, p.desc, sms, p.tile_rows};
-            if (launch_attn_tc(p, kD, sms, true, st) != cudaSuccess) return MOE_ERR_CUDA;
+            if (launch_attn_tc(p, kD, e4m3, sms, true, st) != cudaSuccess) return MOE_ERR_CUDA;
         } else {
             p.tile_rows = 64;
             r = e4m3 ? launch_mma<kD, true, 4>(p, many, true, st) : launch_mma<kD, false, 4>(p, many, true, st);

@@ -20,27 +20,34 @@
 //   - O stays in tensor memory.  Its rows are rescaled only when their maximum
 //     has grown by more than 2^8 since the last time (until then p may exceed 1,
 //     which costs nothing in bf16 and in fp32 sums).
-//   - an item's Q is loaded as soon as the last scores of the item before are
-//     done, and its first scores are issued behind that item's last products, so
-//     that they run while its output is written.
+//   - an item's Q is loaded when the last scores of the item before are done, and
+//     its first scores are issued behind that item's last products, so that they
+//     run while its output is written.
 // A tile holds whole tokens: tile_rows / 2 = group * floor(128 / group) rows.
-// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1 and the output, 8 and 11 issue
-// the MMAs of tile 0 and 1 (apart, because a wait of one must not hold up the
-// other), 9 loads K and V, 10 loads Q.  K and V
-// blocks share one ring of slots in the order K0 V0 K1 V1 ...; a block is put
-// together from one TMA box per page and 64 columns, whose page ids the 32 lanes
-// of the load warp read side by side.
+// Warp roles: 0-3 and 4-7 softmax of tile 0 and 1 and the output, 8 and 9 issue the
+// MMAs of tile 0 and 1 (apart, because a wait of one must not hold up the other)
+// and load its Q.  K and V blocks share one ring of slots in the order K0 V0 K1 V1
+// ...  Three ways to fill it:
+//   kLoadTma    bf16 cache whose pages a block is made of, or that are made of
+//               blocks: warp 10 issues one TMA box per page and 64 columns, whose
+//               page ids its lanes read side by side;
+//   kLoadCopy   any other page size: warps 12-15 copy rows with cp.async, and hand a
+//               block over once its copies have landed;
+//   kLoadCodes  E4M3 cache: warps 12-15 bring 32 rows each through registers, K
+//               converted to bf16 and V to fp16 on the way.
 #include <mutex>
 
-#include <cuda_bf16.h>
-
+#include "paged_mma.cuh"
 #include "paged_work.cuh"
 
 namespace moe {
 
-template <int kD>
+// How K and V get into shared memory.
+enum { kLoadTma = 0, kLoadCopy = 1, kLoadCodes = 2 };
+
+template <int kD, int kLoad>
 struct TcCfg {
-    static constexpr int kThreads = 384, kBlk = 128;
+    static constexpr int kThreads = kLoad == kLoadTma ? 384 : 512, kBlk = 128;
     static constexpr int kHalf = 128 * 128;                  // bytes of 128 rows x 64 columns
     static constexpr int kHalves = kD / 64;
     static constexpr int kTile = kHalves * kHalf;            // 128 rows x D
@@ -129,13 +136,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ float tc_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -143,21 +143,49 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-__device__ __forceinline__ uint32_t tc_bf16x2(float a, float b)
+// Two fp16 values that came from E4M3 codes as bf16, exactly.
+__device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h)
 {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&r);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return bf16x2_of(f.x, f.y);
 }
 
-template <int kD>
-__global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
+// 16-code chunk `chunk` of rows row, row + kStep, ... into an operand tile, as bf16
+// or fp16, both exactly.  Lanes of the second half of the columns start with their
+// odd 16 bytes, so that the 8 lanes of a row hit 8 different bank groups.
+template <int kHalf, int kStep, bool kBf16, int kN>
+__device__ __forceinline__ void put_codes(uint8_t *tile, int row, int chunk, const uint4 (&from)[kN])
+{
+    uint8_t *dst = tile + (chunk >> 2) * kHalf;
+    const int k = 2 * (chunk & 3), e0 = chunk >> 2 & 1;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int r = row + i * kStep;
+        const uint32_t ww[4] = {from[i].x, from[i].y, from[i].z, from[i].w};
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f16x4_of_e4m3(ww[j], x[2 * j], x[2 * j + 1]);
+            if (kBf16) {
+                x[2 * j] = bf16x2_of_f16x2(x[2 * j]);
+                x[2 * j + 1] = bf16x2_of_f16x2(x[2 * j + 1]);
+            }
+        }
+        const uint4 even = make_uint4(x[0], x[1], x[2], x[3]), odd = make_uint4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<uint4 *>(dst + r * 128 + ((k + e0) ^ (r & 7)) * 16) = e0 ? odd : even;
+        *reinterpret_cast<uint4 *>(dst + r * 128 + ((k + 1 - e0) ^ (r & 7)) * 16) = e0 ? even : odd;
+    }
+}
+
+template <int kD, int kLoad>
+__global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
     paged_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v, const AttnParams p, int box_rows)
 {
-    using C = TcCfg<kD>;
+    using C = TcCfg<kD, kLoad>;
     constexpr int kBlk = C::kBlk, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_full[kSlots], s_empty[kSlots], s_qfull[2], s_qempty[2], s_sfull[2][2], s_pfull[2][2],
+    __shared__ uint64_t s_full[kSlots], s_empty[kSlots], s_qfull[2], s_sfull[2][2], s_pfull[2][2],
         s_pv[2][2], s_drain[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
@@ -168,12 +196,11 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&s_full[i]), kLoad == kLoadTma ? 1 : 4);     // the load warps
             mbar_init(smem_u32(&s_empty[i]), 2);             // both tiles
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&s_qfull[t]), 1);
-            mbar_init(smem_u32(&s_qempty[t]), 1);
             for (int x = 0; x < 2; ++x) {
                 mbar_init(smem_u32(&s_sfull[t][x]), 1);
                 mbar_init(smem_u32(&s_pfull[t][x]), 4);
@@ -214,37 +241,11 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
     };
     const int tile = p.tile_rows >> 1;                       // rows of a tile, at most 128
     long long left = n_blocks;
-    // 12 warps x 168 registers at launch = 8 x 216 + 4 x 72
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 10) {
-        // ------------------------------------------------------------ Q loads
-        uint32_t n_fill[2] = {0, 0};
-        bool ok = true;
-        const uint64_t policy = policy_evict_normal();
-        while (left > 0 && ok) {
-            const int rows = cur.rows(p), tok = cur.r.qs + cur.row0(p) / p.group;
-            for (int t = 0; t < 2 && t * tile < rows && ok; ++t) {
-                ok = wait(&s_qempty[t], (n_fill[t] & 1u) ^ 1u);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&s_qfull[t]);
-                    mbar_arrive_expect_tx(bar, C::kHalves * tile * 128);
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_3d(smem_u32(s_q) + t * C::kTile + h * C::kHalf, &tm_q, bar, 64 * h, cur.kvh * p.group,
-                                    tok + t * (tile / p.group), policy);
-                }
-                __syncwarp();
-                ++n_fill[t];
-            }
-            left -= min(left, static_cast<long long>(cur.nblk - cur.blk));
-            if (left > 0) cur.next_item(p);
-        }
-        volatile int no_abort = 0;                           // the last copies land before the CTA leaves
-        for (int t = 0; t < 2 && !ok; ++t)
-            if (n_fill[t]) mbar_wait(smem_u32(&s_qfull[t]), (n_fill[t] - 1) & 1u, &no_abort);
-    } else if (warp == 9) {
-        // ---------------------------------------------------- K and V loads
+    // 16 warps x 128 registers at launch = 8 x 152 + 8 x 104: a softmax thread holds
+    // 64 scores
+    if (kLoad != kLoadTma && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (kLoad == kLoadTma && warp == 10) {
+        // ------------------------------------------------ K and V loads by TMA
         // lane: box of rows row .. row + box_rows - 1 of the block, columns 64 h ..
         const int boxes = kBlk / box_rows;
         const int h = lane / boxes, row = lane % boxes * box_rows;
@@ -300,10 +301,123 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
             for (uint32_t i = n_fill > kSlots ? n_fill - kSlots : 0; i < n_fill; ++i)
                 mbar_wait(smem_u32(&s_full[i % kSlots]), (i / kSlots) & 1u, &no_abort);
         }
-    } else {
-        // ------------------------------------------------- MMAs of tile t
-        const int t = warp == 8 ? 0 : 1;
-        const uint32_t idesc_s = idesc_make(1, 128, 64), idesc_o = idesc_make(1, 128, kD) | (1u << 16);
+    } else if (kLoad != kLoadTma && warp >= 12) {
+        // ---------------------------- K and V loads, 32 rows of a block a warp
+        // Lane r looks up row r's page: any page size; keys behind the last one, or
+        // on a page outside the cache, become zeros.
+        constexpr int esz = kLoad == kLoadCodes ? 1 : 2, kPerRow = kD * esz / 16, kAtOnce = 32 / kPerRow, kCopies = 32 / kAtOnce;
+        const int first = 32 * (warp - 12), sub = lane / kPerRow, chunk = lane % kPerRow;
+        bool bad = false, ok = true;
+        int slot = 0;
+        uint32_t phase = 0;
+        auto look_up = [&]() -> long long {                  // the row's place in bytes, -1: none
+            const int key = cur.blk * kBlk + first + lane;
+            if (key >= cur.r.kv) return -1;
+            const int col = key / p.page_size;
+            const int id = __ldg(p.table + static_cast<long long>(cur.b) * p.max_pages + col);
+            if (id < 0 || id >= p.num_pages) {
+                bad = true;
+                return -1;
+            }
+            return (id * p.page_stride + (static_cast<long long>(key - col * p.page_size) * p.n_kv + cur.kvh) * kD) * esz;
+        };
+        auto landed = [&](int at) {                          // a slot's rows are written: hand them over
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_full[at]));
+        };
+        auto step = [&]() {
+            if (++slot == kSlots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        long long off = look_up();
+        auto advance = [&]() -> long long {                  // the next block's place
+            if (--left == 0) return -1;
+            if (++cur.blk == cur.nblk) cur.next_item(p);
+            return look_up();
+        };
+        if constexpr (kLoad == kLoadCopy) {
+            int open0 = -1, open1 = -1;                      // slots whose copies are under way, oldest first
+            auto flush = [&]() {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (open0 >= 0) landed(open0);
+                if (open1 >= 0) landed(open1);
+                open0 = open1 = -1;
+            };
+            while (left > 0 && ok) {
+                const long long next = advance();
+#pragma unroll
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    // a slot that is not free yet may be waiting for copies not handed over
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&s_empty[slot]), phase ^ 1u))) {
+                        flush();
+                        ok = wait(&s_empty[slot], phase ^ 1u);
+                        if (!ok) break;
+                    }
+                    const uint8_t *cache = static_cast<const uint8_t *>(kv ? p.v_cache : p.k_cache);
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        const long long o = __shfl_sync(0xffffffffu, off, i * kAtOnce + sub);
+                        const int r = first + i * kAtOnce + sub;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         ring + slot * C::kTile + (chunk >> 3) * C::kHalf + r * 128 + ((chunk & 7) ^ (r & 7)) * 16),
+                                     "l"(cache + (o < 0 ? 0 : o) + chunk * 16), "r"(o < 0 ? 0 : 16)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (open1 >= 0) {
+                        asm volatile("cp.async.wait_group 2;" ::: "memory");
+                        landed(open0);
+                        open0 = open1;
+                        open1 = slot;
+                    } else if (open0 >= 0) {
+                        open1 = slot;
+                    } else {
+                        open0 = slot;
+                    }
+                    step();
+                }
+                off = next;
+            }
+            flush();
+        } else if constexpr (kLoad == kLoadCodes) {
+            // through registers, a fill ahead; K becomes bf16 (like q), V fp16 (like
+            // p), both exactly
+            uint4 wk[kCopies], wv[kCopies];
+            auto load = [&](const void *cache, long long from, uint4 (&to)[kCopies]) {
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const long long o = __shfl_sync(0xffffffffu, from, i * kAtOnce + sub);
+                    to[i] = o < 0 ? make_uint4(0, 0, 0, 0)
+                                  : __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(cache) + o + chunk * 16));
+                }
+            };
+            load(p.k_cache, off, wk);
+            while (left > 0) {
+                const long long next = advance();
+                load(p.v_cache, off, wv);
+                ok = wait(&s_empty[slot], phase ^ 1u);
+                if (!ok) break;
+                put_codes<C::kHalf, kAtOnce, true>(smem + 2 * C::kTile + slot * C::kTile, first + sub, chunk, wk);
+                landed(slot);
+                step();
+                load(p.k_cache, next, wk);
+                ok = wait(&s_empty[slot], phase ^ 1u);
+                if (!ok) break;
+                put_codes<C::kHalf, kAtOnce, false>(smem + 2 * C::kTile + slot * C::kTile, first + sub, chunk, wv);
+                landed(slot);
+                step();
+                off = next;
+            }
+        }
+        if (bad && p.status) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+    } else if (warp == 8 || warp == 9) {
+        // ------------------------------------- MMAs of tile t, and its Q
+        const int t = warp - 8;
+        // P and V are bf16, with a cache of codes fp16; V's rows are the second product's K
+        const uint32_t idesc_s = idesc_make(1, 128, 64), idesc_o = idesc_make(kLoad == kLoadCodes ? 0 : 1, 128, kD) | (1u << 16);
         const uint32_t q0 = smem_u32(s_q) + t * C::kTile;
         const uint32_t ts = tmem + C::kColS + 128 * t, to = tmem + C::kColO + 128 * t;
         int slot = 0;                                        // the next fill to wait for
@@ -329,28 +443,43 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                 mma_commit(smem_u32(&s_sfull[t][half]));
             }
         };
+        uint32_t q_under_way = 0;
+        const uint64_t policy = policy_evict_normal();
+        auto load_q = [&](const Cursor<0, kBlk> &at) {       // the tile's rows of an item
+            if (t * tile >= at.rows(p)) return;
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(&s_qfull[t]);
+                mbar_arrive_expect_tx(bar, C::kHalves * tile * 128);
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(q0 + h * C::kHalf, &tm_q, bar, 64 * h, at.kvh * p.group,
+                                at.r.qs + (at.row0(p) + t * tile) / p.group, policy);
+            }
+            __syncwarp();
+            q_under_way = 1;
+        };
+        load_q(cur);
         while (left > 0 && ok) {
             const int n = static_cast<int>(min(left, static_cast<long long>(cur.nblk - cur.blk)));
+            Cursor<0, kBlk> nxt = cur;
+            if (left > n) nxt.next_item(p);
             if (t * tile < cur.rows(p)) {
                 int kslot = next_fill();
                 if (!ok) break;
                 ok = wait(&s_qfull[t], qphase);
                 if (!ok) break;
                 qphase ^= 1u;
+                q_under_way = 0;
                 tc_fence_after();
                 scores(kslot, 0);
                 scores(kslot, 1);
-                if (elect_one()) {
-                    mma_commit(smem_u32(&s_empty[kslot]));
-                    if (n == 1) mma_commit(smem_u32(&s_qempty[t]));
-                }
+                if (elect_one()) mma_commit(smem_u32(&s_empty[kslot]));
                 for (int j = 0; j < n && ok; ++j) {
                     const int vslot = next_fill();
                     if (!ok) break;
                     // values behind the last key must not reach the product: 0 x NaN
                     // (both tiles' warps write the same zeros)
                     const int valid = cur.r.kv - (cur.blk + j) * kBlk;
-                    if (valid < kBlk) {
+                    if (kLoad == kLoadTma && valid < kBlk) {
                         uint8_t *v = smem + 2 * C::kTile + vslot * C::kTile;
                         const int from = valid < 0 ? 0 : valid;
                         for (int x = from * 8 + lane; x < kBlk * 8; x += 32)
@@ -365,6 +494,8 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                         ok = wait(&s_pfull[t][half], pphase);
                         if (!ok) break;
                         tc_fence_after();
+                        // the item's last scores are done: its Q may go
+                        if (half == 1 && j + 1 == n && left > n) load_q(nxt);
                         if (elect_one()) {
                             const uint32_t b = ring + vslot * C::kTile + half * 8192;
 #pragma unroll
@@ -380,10 +511,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                                 if (!ok) break;
                             }
                             scores(kslot, half);
-                            if (half == 1 && elect_one()) {
-                                mma_commit(smem_u32(&s_empty[kslot]));
-                                if (j + 2 == n) mma_commit(smem_u32(&s_qempty[t]));
-                            }
+                            if (half == 1 && elect_one()) mma_commit(smem_u32(&s_empty[kslot]));
                         }
                     }
                     pphase ^= 1u;
@@ -394,23 +522,24 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                     const int f = next_fill();
                     if (ok && lane == 0) mbar_arrive(smem_u32(&s_empty[f]));
                 }
+                if (ok && left > n) load_q(nxt);
             }
             if (!ok) break;
             left -= n;
-            if (left > 0) cur.next_item(p);
+            cur = nxt;
         }
         if (!ok) {
             if (elect_one()) {
                 volatile int no_abort = 0;
+                if (q_under_way) mbar_wait(smem_u32(&s_qfull[t]), qphase, &no_abort);
                 mma_commit(smem_u32(&s_drain[t]));
                 mbar_wait(smem_u32(&s_drain[t]), 0, &no_abort);
             }
             __syncwarp();
         }
-    }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    } else if (warp < 8) {
         // ------------------------------------------- softmax of tile t, a row each
+        if (kLoad != kLoadTma) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // lane 32 (warp mod 4) in bits 16..
         const uint32_t ts = tmem + C::kColS + 128 * t + lanes, to = tmem + C::kColO + 128 * t + lanes;
@@ -456,7 +585,7 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
                     const float mn = max3(max3(m, top[0], top[1]), max3(top[2], top[3], top[4]), max3(top[5], top[6], top[7]));
                     if (__any_sync(0xffffffffu, (mn - m) * mult > kRescale)) {
                         // (mn = m = -inf gives NaN above and does not count)
-                        const float f = m == -INFINITY ? 0.0f : tc_exp2((m - mn) * mult);
+                        const float f = m == -INFINITY ? 0.0f : exp2_fast((m - mn) * mult);
                         m = mn;
                         l *= f;
                         if (x > 0) {
@@ -481,9 +610,9 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
                         const float2 v = __ffma2_rn(make_float2(s[i], s[i + 1]), mult2, base2);
-                        const float2 e = make_float2(tc_exp2(v.x), tc_exp2(v.y));
+                        const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
                         sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
-                        w[i >> 1] = tc_bf16x2(e.x, e.y);
+                        w[i >> 1] = kLoad == kLoadCodes ? f16x2_of(e.x, e.y) : bf16x2_of(e.x, e.y);
                     }
                     tmem_st16(ts + 64 * half, w);
                     tmem_st16(ts + 64 * half + 16, w + 16);
@@ -509,8 +638,8 @@ __global__ void __launch_bounds__(TcCfg<kD>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; i += 8)
                                 *reinterpret_cast<uint4 *>(dst + c + i) =
-                                    make_uint4(tc_bf16x2(o[i] * inv, o[i + 1] * inv), tc_bf16x2(o[i + 2] * inv, o[i + 3] * inv),
-                                               tc_bf16x2(o[i + 4] * inv, o[i + 5] * inv), tc_bf16x2(o[i + 6] * inv, o[i + 7] * inv));
+                                    make_uint4(bf16x2_of(o[i] * inv, o[i + 1] * inv), bf16x2_of(o[i + 2] * inv, o[i + 3] * inv),
+                                               bf16x2_of(o[i + 4] * inv, o[i + 5] * inv), bf16x2_of(o[i + 6] * inv, o[i + 7] * inv));
                         }
                     }
                 } else {
@@ -617,14 +746,10 @@ static bool query_map(CUtensorMap *m, const AttnParams &p, int kD)
 
 bool attn_tc_takes(const moe_attn_shape_t &s)
 {
-    // a block of 128 keys is made of whole boxes: pages that divide it (the
-    // 1024-byte swizzle pattern wants at least 8 rows), or that it divides; a
-    // tile of 128 rows holds whole tokens; and the maximum of q.k is that of the
-    // scores.  A tensor map's strides are below 2^40 bytes.
+    // a tile of 128 rows holds whole tokens, and the maximum of q.k is that of the
+    // scores; the query map's stride is below 2^40 bytes
     if (s.head_dim != 64 && s.head_dim != 128) return false;
-    if (s.cache_dtype != MOE_BF16 || s.n_heads / s.n_kv_heads > 128 || s.scale < 0.0f) return false;
-    if (s.q_stride >= 1ll << 39 || s.page_stride >= 1ll << 39) return false;
-    return (s.page_size >= 8 && 128 % s.page_size == 0) || s.page_size % 128 == 0;
+    return s.n_heads / s.n_kv_heads <= 128 && s.scale >= 0.0f && s.q_stride < 1ll << 39;
 }
 
 int attn_tc_rows(const moe_attn_shape_t &s)
@@ -633,23 +758,35 @@ int attn_tc_rows(const moe_attn_shape_t &s)
     return 2 * group * (128 / group);
 }
 
-cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int sms, bool chained, cudaStream_t st)
+template <int kD, int kLoad>
+static cudaError_t launch_tc(const AttnParams &p, int sms, bool chained, cudaStream_t st)
 {
+    using C = TcCfg<kD, kLoad>;
     static PerDeviceOnce once;
-    once([] {
-        cudaFuncSetAttribute(paged_attention_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<64>::kSmem);
-        cudaFuncSetAttribute(paged_attention_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<128>::kSmem);
-    });
+    once([] { cudaFuncSetAttribute(paged_attention_tc_kernel<kD, kLoad>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     const int box_rows = p.page_size < 128 ? p.page_size : 128;
     CUtensorMap q, k, v;
-    if (!query_map(&q, p, head_dim) || !cache_map(&k, p.k_cache, p, head_dim, box_rows) ||
-        !cache_map(&v, p.v_cache, p, head_dim, box_rows))
+    if (!query_map(&q, p, kD)) return cudaErrorInvalidValue;
+    k = v = q;
+    if (kLoad == kLoadTma && (!cache_map(&k, p.k_cache, p, kD, box_rows) || !cache_map(&v, p.v_cache, p, kD, box_rows)))
         return cudaErrorInvalidValue;
+    return launch_kernel(paged_attention_tc_kernel<kD, kLoad>, dim3(sms), dim3(C::kThreads), C::kSmem, st, chained, q, k, v, p, box_rows);
+}
+
+cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, bool e4m3, int sms, bool chained, cudaStream_t st)
+{
+    // TMA takes a block as whole boxes: pages that divide it, or that it divides.
+#ifndef TC_PAGE
+#define TC_PAGE 8
+#endif
+    const bool boxes = ((p.page_size >= TC_PAGE && 128 % p.page_size == 0) || p.page_size % 128 == 0) && p.page_stride < 1ll << 39;
     if (head_dim == 64)
-        return launch_kernel(paged_attention_tc_kernel<64>, dim3(sms), dim3(TcCfg<64>::kThreads), TcCfg<64>::kSmem, st, chained, q, k, v,
-                             p, box_rows);
-    return launch_kernel(paged_attention_tc_kernel<128>, dim3(sms), dim3(TcCfg<128>::kThreads), TcCfg<128>::kSmem, st, chained, q, k, v, p,
-                         box_rows);
+        return e4m3    ? launch_tc<64, kLoadCodes>(p, sms, chained, st)
+               : boxes ? launch_tc<64, kLoadTma>(p, sms, chained, st)
+                       : launch_tc<64, kLoadCopy>(p, sms, chained, st);
+    return e4m3    ? launch_tc<128, kLoadCodes>(p, sms, chained, st)
+           : boxes ? launch_tc<128, kLoadTma>(p, sms, chained, st)
+                   : launch_tc<128, kLoadCopy>(p, sms, chained, st);
 }
 
 }  // namespace moe

@@ -333,7 +333,7 @@ struct Split {
 // its launch with one CTA (and range) per SM.
 bool attn_tc_takes(const moe_attn_shape_t &s);
 int attn_tc_rows(const moe_attn_shape_t &s);
-cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, int sms, bool chained, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, bool e4m3, int sms, bool chained, cudaStream_t st);
 
 // The decode kernel, one CTA of kDecodeWarps ranges per SM.
 constexpr int kDecodeWarps = 8;
