@@ -33,8 +33,8 @@
 //               page ids its lanes read side by side;
 //   kLoadCopy   any other page size: warps 12-15 copy rows with cp.async, and hand a
 //               block over once its copies have landed;
-//   kLoadCodes  E4M3 cache: warps 12-15 bring 32 rows each through registers, K
-//               converted to bf16 and V to fp16 on the way.
+//   kLoadCodes  E4M3 cache: warps 12-15 copy codes ahead and convert them, K to bf16
+//               and V to fp16, into the ring.
 #include <mutex>
 
 #include "paged_mma.cuh"
@@ -51,8 +51,10 @@ struct TcCfg {
     static constexpr int kHalf = 128 * 128;                  // bytes of 128 rows x 64 columns
     static constexpr int kHalves = kD / 64;
     static constexpr int kTile = kHalves * kHalf;            // 128 rows x D
-    static constexpr int kSlots = kD == 128 ? 5 : 8;
-    static constexpr int kSmem = 2 * kTile + kSlots * kTile + 1024;   // + alignment
+    static constexpr int kSlots = kD == 64 ? 8 : kLoad == kLoadCodes ? 4 : 5;
+    // codes on their way: kDepth blocks of K or V
+    static constexpr int kDepth = kD == 64 ? 4 : 2, kRaw = kLoad == kLoadCodes ? kDepth * 128 * kD : 0;
+    static constexpr int kSmem = 2 * kTile + kSlots * kTile + kRaw + 1024;   // + alignment
     static constexpr int kColS = 0, kColO = 256;             // tensor-memory columns, tile t at + 128 t
 };
 
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         };
         long long off = look_up();
         auto advance = [&]() -> long long {                  // the next block's place
-            if (--left == 0) return -1;
+            if (left == 0 || --left == 0) return -1;
             if (++cur.blk == cur.nblk) cur.next_item(p);
             return look_up();
         };
@@ -383,34 +385,45 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
             }
             flush();
         } else if constexpr (kLoad == kLoadCodes) {
-            // through registers, a fill ahead; K becomes bf16 (like q), V fp16 (like
-            // p), both exactly
-            uint4 wk[kCopies], wv[kCopies];
-            auto load = [&](const void *cache, long long from, uint4 (&to)[kCopies]) {
+            // The codes of K or V blocks are copied kDepth ahead; K becomes bf16
+            // (like q), V fp16 (like p), both exactly.  A lane converts what it
+            // copied itself.
+            const uint32_t raw = ring + kSlots * C::kTile + first * kD + lane * 16;
+            long long todo = 2 * left;                       // K and V blocks to convert
+            int fill = 0;                                    // of the one to copy next, mod kDepth
+            bool v_next = false;
+            auto copy = [&]() {
+                const uint8_t *cache = static_cast<const uint8_t *>(v_next ? p.v_cache : p.k_cache);
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i) {
-                    const long long o = __shfl_sync(0xffffffffu, from, i * kAtOnce + sub);
-                    to[i] = o < 0 ? make_uint4(0, 0, 0, 0)
-                                  : __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(cache) + o + chunk * 16));
+                    const long long o = __shfl_sync(0xffffffffu, off, i * kAtOnce + sub);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + fill * (128 * kD) + i * 512),
+                                 "l"(cache + (o < 0 ? 0 : o) + chunk * 16), "r"(o < 0 ? 0 : 16)
+                                 : "memory");
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (++fill == C::kDepth) fill = 0;
+                if (v_next) off = advance();
+                v_next = !v_next;
             };
-            load(p.k_cache, off, wk);
-            while (left > 0) {
-                const long long next = advance();
-                load(p.v_cache, off, wv);
+#pragma unroll
+            for (int i = 0; i < C::kDepth; ++i) copy();
+            for (bool v_now = false; todo > 0; --todo, v_now = !v_now) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::kDepth - 1) : "memory");
+                uint4 w[kCopies];
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(smem + (raw - smem_u32(smem)) + fill * (128 * kD) + i * 512);
                 ok = wait(&s_empty[slot], phase ^ 1u);
                 if (!ok) break;
-                put_codes<C::kHalf, kAtOnce, true>(smem + 2 * C::kTile + slot * C::kTile, first + sub, chunk, wk);
+                copy();
+                uint8_t *to = smem + 2 * C::kTile + slot * C::kTile;
+                if (!v_now) put_codes<C::kHalf, kAtOnce, true>(to, first + sub, chunk, w);
+                else put_codes<C::kHalf, kAtOnce, false>(to, first + sub, chunk, w);
                 landed(slot);
                 step();
-                load(p.k_cache, next, wk);
-                ok = wait(&s_empty[slot], phase ^ 1u);
-                if (!ok) break;
-                put_codes<C::kHalf, kAtOnce, false>(smem + 2 * C::kTile + slot * C::kTile, first + sub, chunk, wv);
-                landed(slot);
-                step();
-                off = next;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         if (bad && p.status) set_status(p.status, MOE_ERR_DEVICE_CHECK);
     } else if (warp == 8 || warp == 9) {
