@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             id_key = ld.blk * kBlk + tid;
             id_in = id_key < ld.r.kv;
             id_kvh = ld.kvh;
-            id_page = id_in ? __ldg(p.table + static_cast<long long>(ld.b) * p.max_pages + id_key / p.page_size) : 0;
+            id_page = id_in ? __ldg(p.table + static_cast<long long>(ld.b) * p.max_pages + p.by_page.div(id_key)) : 0;
             if (--ld_left > 0 && ++ld.blk == ld.nblk) ld.next_item(p);
         } else {
             id_in = false;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
         long long off = -1;
         if (id_in) {
             if (id_page >= 0 && id_page < p.num_pages)
-                off = id_page * p.page_stride + (static_cast<long long>(id_key % p.page_size) * p.n_kv + id_kvh) * kD;
+                off = id_page * p.page_stride + (static_cast<long long>(id_key - p.by_page.div(id_key) * p.page_size) * p.n_kv + id_kvh) * kD;
             else
                 bad = true;
         }
@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             const int r = tid / kTpr, part = tid % kTpr;
             const int rows = cur.rows(p);
             const int grow = cur.row0(p) + r;
-            const int tok = grow / p.group;
+            const int tok = p.by_group.div(grow);
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
                                        static_cast<long long>(cur.r.qs + tok) * p.q_stride +
-                                       static_cast<long long>(cur.kvh * p.group + grow % p.group) * kD;
+                                       static_cast<long long>(cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
             uint4 w[kCpt];
 #pragma unroll
             for (int i = 0; i < kCpt; ++i)
@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                         if (whole) {
                             const float inv = l[h] > 0.0f ? p.v_scale / l[h] : l[h] == 0.0f ? 0.0f : l[h];
                             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                                 (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
-                                                  cur.kvh * p.group + grow % p.group) * kD;
+                                                 (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
+                                                  cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
 #pragma unroll
                             for (int i = 0; i < kD / 8; ++i) {
                                 if constexpr (kE4m3) {
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                         } else {
 #pragma unroll
                             for (int i = 0; i < kD / 8; ++i) {
-                                part[r * kD + col(i, 0)] = o[i][2 * h];
-                                part[r * kD + col(i, 1)] = o[i][2 * h + 1];
+                                part[many_at(kRows, r, col(i, 0))] = o[i][2 * h];
+                                part[many_at(kRows, r, col(i, 1))] = o[i][2 * h + 1];
                             }
                             if (cq == 0) {
                                 part[kRows * kD + r] = m[h];
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                         const float inv = lt > 0.0f ? p.v_scale / lt : lt == 0.0f ? 0.0f : lt;
                         const int grow = cur.row0(p) + r;
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                             (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
-                                              cur.kvh * p.group + grow % p.group) * kD + c;
+                                             (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
+                                              cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD + c;
                         *reinterpret_cast<uint4 *>(dst) =
                             make_uint4(bf16x2_of(v[0] * inv, v[1] * inv), bf16x2_of(v[2] * inv, v[3] * inv),
                                        bf16x2_of(v[4] * inv, v[5] * inv), bf16x2_of(v[6] * inv, v[7] * inv));
@@ -561,10 +561,67 @@ __device__ __forceinline__ void put_row(const AttnParams &p, const AttnDesc &d, 
     const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
     const int grow = d.row0 + r;
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                         (static_cast<long long>(d.qs + grow / p.group) * p.n_heads + d.kvh * p.group + grow % p.group) * kD +
+                         (static_cast<long long>(d.qs + p.by_group.div(grow)) * p.n_heads + d.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD +
                          (threadIdx.x & 31) * kE;
 #pragma unroll
     for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// The same for items of many rows (see many_at): two adjacent rows a lane, kD / 4
+// lanes across them where that is less than a warp.
+template <int kD>
+__device__ __forceinline__ void join_rows(const AttnParams &p, const AttnParts &from, int c, int row0, int behind)
+{
+    constexpr int kAcross = kD / 4 < 32 ? kD / 4 : 32, kC = kD / 4 / kAcross, kStep = 2 * (32 / kAcross);
+    const AttnDesc d = from.desc[c];
+    if (d.parts < 2) return;
+    const int lane = threadIdx.x & 31, x = lane % kAcross;
+    const long long stride = static_cast<long long>(from.rows) * (kD + 2);
+    auto part = [&](int k) { return from.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
+    for (int r0 = row0 + (threadIdx.x >> 5) * kStep; r0 < min(d.rows, behind); r0 += 8 * kStep) {
+        const int r = r0 + 2 * (lane / kAcross), at_m = from.rows * kD + r, at_l = at_m + from.rows;
+        float base[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float4 acc[2][kC];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < kC; ++i) acc[j][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // the rows are even, so that both have a place even where the second is none of the item's
+#pragma unroll 4
+        for (int k = 0; k < d.parts; ++k) {
+            base[0] = fmaxf(base[0], part(k)[at_m]);
+            base[1] = fmaxf(base[1], part(k)[at_m + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (base[j] == -INFINITY) base[j] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < d.parts; ++k) {
+            const float *q = part(k);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float f = exp2_fast(q[at_m + j] - base[j]);
+                l[j] += f * q[at_l + j];
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    const float4 v = *reinterpret_cast<const float4 *>(q + many_at(from.rows, r + j, 4 * (x + i * kAcross)));
+                    acc[j][i] = make_float4(acc[j][i].x + f * v.x, acc[j][i].y + f * v.y, acc[j][i].z + f * v.z, acc[j][i].w + f * v.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (r + j >= d.rows) continue;
+            const float inv = l[j] > 0.0f ? p.v_scale / l[j] : l[j] == 0.0f ? 0.0f : l[j];
+            const int grow = d.row0 + r + j, tok = p.by_group.div(grow);
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                 (static_cast<long long>(d.qs + tok) * p.n_heads + d.kvh * p.group + (grow - tok * p.group)) * kD;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+                *reinterpret_cast<uint2 *>(dst + 4 * (x + i * kAcross)) =
+                    make_uint2(bf16x2_of(acc[j][i].x * inv, acc[j][i].y * inv), bf16x2_of(acc[j][i].z * inv, acc[j][i].w * inv));
+        }
+    }
 }
 
 // Joins the parts of the items that lie in several ranges, of one or two kernels.
@@ -572,7 +629,7 @@ __device__ __forceinline__ void put_row(const AttnParams &p, const AttnDesc &d, 
 // ranges and every fourth row of the items that they start; a warp joins its
 // item's row alone, and where an item has many parts (few requests, long
 // sequences) the 8 warps share them.  Second kernel (items of many rows): a block
-// has one range and 32 rows of its item, a warp a row.
+// has one range and 32 rows of its item.
 constexpr int kManyParts = 16;
 
 template <int kD>
@@ -585,13 +642,8 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const AttnParams
     float acc[kE], l;
     grid_dep_wait();
     if (static_cast<int>(blockIdx.x) >= few_blocks) {
-        const int per = (many.rows + 31) / 32, x = blockIdx.x - few_blocks, c = x / per;
-        const AttnDesc d = many.desc[c];
-        if (d.parts < 2) return;
-        for (int r = x % per * 32 + warp; r < min(d.rows, x % per * 32 + 32); r += 8) {
-            join_row<kD>(many, c, d.parts, r, 0, d.parts, acc, l);
-            put_row<kD>(p, d, r, acc, l);
-        }
+        const int per = (many.rows + 31) / 32, x = blockIdx.x - few_blocks, row0 = x % per * 32;
+        join_rows<kD>(p, many, x / per, row0, row0 + 32);
         return;
     }
     const int c0 = blockIdx.x / 4 * 8, y = blockIdx.x % 4;
@@ -718,9 +770,14 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
     p.min_rows = 1;
     p.max_rows = only_few(s) ? 0x7fffffff : kFewRows;
     p.wait_at_end = 0;
-    p.tile_rows = kFewRows;
+    auto items_of = [&](int rows) {
+        p.tile_rows = rows;
+        p.tile_tokens = rows % p.group ? 0 : rows / p.group;
+        p.by_tile.set(rows);
+    };
+    items_of(kFewRows);
     int r;
-    if (attn_decode_takes(s)) {
+    if constexpr (kD <= 128) {
         few = AttnParts{p.part, p.desc, sms * kDecodeWarps, kFewRows};
         if (launch_attn_decode(p, kD, e4m3, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
     } else {
@@ -735,11 +792,11 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         p.max_rows = 0x7fffffff;
         p.wait_at_end = 1;
         if (attn_tc_takes(s)) {
-            p.tile_rows = attn_tc_rows(s);
+            items_of(attn_tc_rows(s));
             many = AttnParts{p.part, p.desc, sms, p.tile_rows};
             if (launch_attn_tc(p, kD, e4m3, sms, true, st) != cudaSuccess) return MOE_ERR_CUDA;
         } else {
-            p.tile_rows = 64;
+            items_of(64);
             r = e4m3 ? launch_mma<kD, true, 4>(p, many, true, st) : launch_mma<kD, false, 4>(p, many, true, st);
             if (r != MOE_OK) return r;
         }
@@ -763,7 +820,7 @@ static int check_attn(const moe_attn_shape_t *shape)
         (s.causal != 0 && s.causal != 1) || s.max_q < 0 || (s.cache_dtype != MOE_BF16 && s.cache_dtype != MOE_E4M3))
         return MOE_ERR_INVALID_ARG;
     if (s.head_dim != 64 && s.head_dim != 128 && s.head_dim != 256) return MOE_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(s.num_pages) * s.page_size > 0x7fffffffll || static_cast<int64_t>(s.num_tokens) * s.n_heads > 0x7fffffffll ||
+    if (static_cast<int64_t>(s.num_pages) * s.page_size > 0x7fffffffll || static_cast<int64_t>(s.num_tokens) * s.n_heads > 0x40000000ll ||
         static_cast<int64_t>(s.max_pages) * s.page_size > 0x40000000ll)
         return MOE_ERR_INVALID_ARG;
     if (s.q_stride && (s.q_stride < static_cast<int64_t>(s.n_heads) * s.head_dim || s.q_stride % 8)) return MOE_ERR_INVALID_ARG;
@@ -819,6 +876,8 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     p.n_kv = s.n_kv_heads;
     p.group = s.n_heads / s.n_kv_heads;
     p.page_size = s.page_size;
+    p.by_group.set(p.group);
+    p.by_page.set(p.page_size);
     p.num_pages = s.num_pages;
     p.max_pages = s.max_pages;
     p.causal = s.causal;

@@ -152,6 +152,20 @@ __device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h)
     return bf16x2_of(f.x, f.y);
 }
 
+// 32 bytes of a lane's own row: one store of a whole sector where the buffer allows
+// it.  A warp's store touches 32 rows, and takes as long whatever it brings to each.
+__device__ __forceinline__ void put_32b(void *dst, const uint32_t (&y)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+                     "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+}
+
 // 16-code chunk `chunk` of rows row, row + kStep, ... into an operand tile, as bf16
 // or fp16, both exactly.  Lanes of the second half of the columns start with their
 // odd 16 bytes, so that the 8 lanes of a row hit 8 different bank groups.
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         auto page_of = [&](const Cursor<0, kBlk> &at) {  // -1: no such key
             const int key = at.blk * kBlk + row;
             if (!mine || key >= at.r.kv) return -1;
-            int id = __ldg(p.table + static_cast<long long>(at.b) * p.max_pages + key / p.page_size);
+            int id = __ldg(p.table + static_cast<long long>(at.b) * p.max_pages + p.by_page.div(key));
             if (id < 0 || id >= p.num_pages) {
                 bad = true;
                 id = p.num_pages;                            // outside the map: zeros
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         int id = page_of(cur);
         bool ok = true;
         while (ok) {
-            const int key = cur.blk * kBlk + row, off = key % p.page_size, kvh = cur.kvh;
+            const int key = cur.blk * kBlk + row, off = key - p.by_page.div(key) * p.page_size, kvh = cur.kvh;
             const int n_box = __popc(__ballot_sync(0xffffffffu, id >= 0));
             int next = -1;
             const bool more = --left > 0;
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         auto look_up = [&]() -> long long {                  // the row's place in bytes, -1: none
             const int key = cur.blk * kBlk + first + lane;
             if (key >= cur.r.kv) return -1;
-            const int col = key / p.page_size;
+            const int col = p.by_page.div(key);
             const int id = __ldg(p.table + static_cast<long long>(cur.b) * p.max_pages + col);
             if (id < 0 || id >= p.num_pages) {
                 bad = true;
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                 mbar_arrive_expect_tx(bar, C::kHalves * tile * 128);
                 for (int h = 0; h < C::kHalves; ++h)
                     tma_load_3d(q0 + h * C::kHalf, &tm_q, bar, 64 * h, at.kvh * p.group,
-                                at.r.qs + (at.row0(p) + t * tile) / p.group, policy);
+                                at.r.qs + p.by_group.div(at.row0(p) + t * tile), policy);
             }
             __syncwarp();
             q_under_way = 1;
@@ -567,8 +581,8 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
             if (t * tile < rows) {
                 const int row = t * tile + r, grow = cur.row0(p) + row;
                 const bool real = r < tile && row < rows;
-                const long long tok = cur.r.qs + grow / p.group;
-                const int head = cur.kvh * p.group + grow % p.group;
+                const long long tok = cur.r.qs + p.by_group.div(grow);
+                const int head = cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group);
                 const int lim = real ? row_limit(p, cur.r, grow) : 0;
                 float m = -INFINITY, l = 0.0f;               // m: largest q.k that O is relative to
                 for (int x = 0; x < 2 * n; ++x) {            // blocks of 64 keys
@@ -642,6 +656,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                 if (last && !continued) {
                     const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (tok * p.n_heads + head) * kD;
+                    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll
                     for (int c = 0; c < kD; c += 32) {
                         float o[32];
@@ -649,10 +664,12 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                         tmem_wait_ld();
                         if (real) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                *reinterpret_cast<uint4 *>(dst + c + i) =
-                                    make_uint4(bf16x2_of(o[i] * inv, o[i + 1] * inv), bf16x2_of(o[i + 2] * inv, o[i + 3] * inv),
-                                               bf16x2_of(o[i + 4] * inv, o[i + 5] * inv), bf16x2_of(o[i + 6] * inv, o[i + 7] * inv));
+                            for (int i = 0; i < 32; i += 16) {
+                                uint32_t y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = bf16x2_of(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
+                                put_32b(dst + c + i, y, wide);
+                            }
                         }
                     }
                 } else {
@@ -665,7 +682,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                         if (real) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4 *>(part + row * kD + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                *reinterpret_cast<float4 *>(part + many_at(p.tile_rows, row, c + i)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
                     }
                     if (real) {

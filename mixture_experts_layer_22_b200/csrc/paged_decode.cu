@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
         for (int j = 0; j < kLook; ++j) {
             const int row = 32 * j + lane, key = ld.blk * kBlk + row;
             if (row >= kBlk || key >= ld.r.kv) continue;
-            const int col = key / p.page_size;
+            const int col = p.by_page.div(key);
             const int id = __ldg(p.table + static_cast<long long>(ld.b) * p.max_pages + col);
             if (id < 0 || id >= p.num_pages) bad = true;
             else off[j] = (id * p.page_stride + (static_cast<long long>(key - col * p.page_size) * p.n_kv + ld.kvh) * kD) * esz;
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
     // column of element e of the accumulator's tile i
     auto col = [&](int i, int e) { return kE4m3 ? 16 * (i >> 1) + 4 * cq + 2 * e + (i & 1) : 8 * i + 2 * cq + e; };
     auto out_row = [&](int grow) {
-        return static_cast<__nv_bfloat16 *>(p.out) + (static_cast<long long>(cur.r.qs + grow / p.group) * p.n_heads +
-                                                      cur.kvh * p.group + grow % p.group) * kD;
+        return static_cast<__nv_bfloat16 *>(p.out) + (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
+                                                      cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
     };
     for (;;) {
         const int n = static_cast<int>(min(n_blocks - begin, static_cast<long long>(cur.nblk - cur.blk)));
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
                 const int r = r_lo + 8 * h, grow = row0 + r;
                 const bool real = r < rows;
                 const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                           static_cast<long long>(cur.r.qs + grow / p.group) * p.q_stride +
-                                           static_cast<long long>(cur.kvh * p.group + grow % p.group) * kD;
+                                           static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.q_stride +
+                                           static_cast<long long>(cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
                 lim[h] = real ? row_limit(p, cur.r, grow) : 0;
                 mult[h] = p.scale_log2;
 #pragma unroll
@@ -363,8 +363,6 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
     copies_wait<0>();
     if (bad && p.status) set_status(p.status, MOE_ERR_DEVICE_CHECK);
 }
-
-bool attn_decode_takes(const moe_attn_shape_t &s) { return s.head_dim == 64 || s.head_dim == 128; }
 
 template <int kD, bool kE4m3>
 static cudaError_t launch_decode(const AttnParams &p, int sms, cudaStream_t st)

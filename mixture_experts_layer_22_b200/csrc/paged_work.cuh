@@ -24,6 +24,10 @@ constexpr int kAttnMaxB = 4096;
 constexpr int kAttnMaxSms = 160;
 constexpr int kAttnMaxUnits = kAttnMaxSms * 8;   // ranges of one kernel: up to 8 warps or 4 CTAs per SM
 
+// Where element d of row r lies in the partial result of an item of many rows: four
+// elements of all rows side by side, since the writers have a row a lane.
+__device__ __forceinline__ int many_at(int rows, int r, int d) { return ((d >> 2) * rows + r) * 4 + (d & 3); }
+
 // What a combine block needs to know of the item that range c starts and does not
 // finish: its parts are (c, slot 1), (c + 1, slot 0), ... (c + parts - 1, slot 0).
 struct AttnDesc {
@@ -51,17 +55,36 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// Division of 0 <= n < 2^31 by a divisor fixed on the host: with 2^s at least the
+// divisor times 2^32 and m = ceil(2^s / d), n m / 2^s exceeds n / d by less than
+// n / 2^s < 1 / d, so the whole part is that of n / d.
+struct FastDiv {
+    unsigned long long m;
+    int s;
+
+    void set(int d)
+    {
+        int log = 0;
+        while ((1ll << log) < d) ++log;
+        s = 32 + log - (log > 31 ? 1 : 0);
+        m = ((1ull << s) - 1) / d + 1;
+    }
+    __device__ __forceinline__ int div(int n) const { return static_cast<int>(static_cast<unsigned long long>(n) * m >> s); }
+};
+
 struct AttnParams {
     const void *q, *k_cache, *v_cache;
     const int32_t *table, *q_start, *kv_len;
     void *out;
     int32_t *status;
-    float *part;          // [G][2][rows * (D + 2)]: sums, then maxima, then totals
+    float *part;          // [G][2][rows * (D + 2)]: sums, then maxima, then totals, of items
     AttnDesc *desc;       // [G]
     long long q_stride, page_stride;
     int B, T, n_heads, n_kv, group, page_size, num_pages, max_pages, causal;
     int min_rows, max_rows;   // this kernel's requests: rows in [min_rows, max_rows]
     int tile_rows;            // query rows of an item
+    int tile_tokens;          // whole tokens of an item, 0 where tokens are cut
+    FastDiv by_group, by_page, by_tile;
     int wait_at_end;          // launched while the kernel before it runs
     float scale_log2, v_scale;
 };
@@ -98,7 +121,7 @@ __device__ __forceinline__ Req attn_request(const AttnParams &p, int b, bool &ba
 __device__ __forceinline__ int row_limit(const AttnParams &p, const Req &r, int row)
 {
     if (!p.causal) return r.kv;
-    const int hi = r.kv - r.n + 1 + row / p.group;
+    const int hi = r.kv - r.n + 1 + p.by_group.div(row);
     return hi < 0 ? 0 : hi;
 }
 
@@ -156,12 +179,12 @@ template <int kRows, int kBlk>
 __device__ __forceinline__ long long request_blocks(const AttnParams &p, const Req &r)
 {
     if (r.n == 0) return 0;
-    const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = (rows + per - 1) / per;
+    const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = p.by_tile.div(rows + per - 1);
     if (!p.causal) return static_cast<long long>(tiles) * tile_blocks<kBlk>(p, r, rows - 1);
     long long s = tile_blocks<kBlk>(p, r, rows - 1);
-    if (per % p.group == 0 && r.kv >= r.n) {
-        // the full tiles see kv - n + (i + 1) per / group keys
-        const int step = per / p.group;
+    if (p.tile_tokens && r.kv >= r.n) {
+        // the full tiles see kv - n + (i + 1) tile_tokens keys
+        const int step = p.tile_tokens;
         if (tiles > 1) s += floor_sum(tiles - 1, kBlk, step, r.kv - r.n + step + kBlk - 1);
     } else {
         for (int i = 0; i < tiles - 1; ++i) s += tile_blocks<kBlk>(p, r, (i + 1) * per - 1);
@@ -183,7 +206,7 @@ struct Cursor {
     }
     __device__ __forceinline__ void enter_request(const AttnParams &p)
     {
-        tiles = (r.n * p.group + item_rows<kRows>(p) - 1) / item_rows<kRows>(p);
+        tiles = p.by_tile.div(r.n * p.group + item_rows<kRows>(p) - 1);
     }
     // On to the next item (warp-collective).  There must be one.
     __device__ __forceinline__ void next_item(const AttnParams &p)
@@ -256,8 +279,8 @@ struct Split {
         G = W < units ? static_cast<int>(W) : units;
         if (unit(0) >= G) return 0;                          // none of the CTA's ranges
         __syncthreads();
-        if (tid < kUnits && unit(tid) < G) {
-            long long at = start(unit(tid));
+        if (warp < kUnits && unit(warp) < G) {
+            long long at = start(unit(warp));
             // the thread in whose requests it lies: the last one with before <= at
             int lo = 0, hi = kThreads;
             while (hi - lo > 1) {
@@ -277,23 +300,24 @@ struct Split {
             }
             const int kvh = static_cast<int>(div_ll(at, per_head));
             at -= per_head * kvh;
-            const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = (rows + per - 1) / per;
+            const int per = item_rows<kRows>(p), rows = r.n * p.group, tiles = p.by_tile.div(rows + per - 1);
             int tile = 0;
             if (!p.causal) {
                 const int nb = tile_blocks<kBlk>(p, r, rows - 1);
                 tile = static_cast<int>(div_ll(at, nb));
                 at -= static_cast<long long>(tile) * nb;
-            } else if (per % p.group == 0 && r.kv >= r.n) {
-                const int step = per / p.group;
-                const long long base = r.kv - r.n + step + kBlk - 1;
-                int first = 0, behind = tiles;               // blocks before `first` <= at < blocks before `behind`
-                while (behind - first > 1) {
-                    const int mid = (first + behind) >> 1;
-                    if (floor_sum(mid, kBlk, step, base) <= at) first = mid;
-                    else behind = mid;
+            } else if (p.tile_tokens && r.kv >= r.n) {
+                // the last tile with no more than `at` blocks before it, 32 tries at once
+                const long long base = r.kv - r.n + p.tile_tokens + kBlk - 1;
+                int behind = tiles;
+                while (behind - tile > 1) {
+                    const int step = (behind - tile + 31) / 32, probe = tile + lane * step;
+                    const bool fits = lane == 0 || (probe < behind && floor_sum(probe, kBlk, p.tile_tokens, base) <= at);
+                    const int last = 31 - __clz(__ballot_sync(0xffffffffu, fits));
+                    tile += last * step;
+                    behind = min(behind, tile + step);
                 }
-                tile = first;
-                if (first > 0) at -= floor_sum(first, kBlk, step, base);
+                if (tile > 0) at -= floor_sum(tile, kBlk, p.tile_tokens, base);
             } else {
                 for (;; ++tile) {
                     const int nb = tile_blocks<kBlk>(p, r, min((tile + 1) * per, rows) - 1);
@@ -301,10 +325,12 @@ struct Split {
                     at -= nb;
                 }
             }
-            s_at[tid][0] = b;
-            s_at[tid][1] = kvh;
-            s_at[tid][2] = tile;
-            s_at[tid][3] = static_cast<int>(at);
+            if (lane == 0) {
+                s_at[warp][0] = b;
+                s_at[warp][1] = kvh;
+                s_at[warp][2] = tile;
+                s_at[warp][3] = static_cast<int>(at);
+            }
         }
         __syncthreads();
         const int k = kUnits > 1 ? warp : 0;
@@ -335,9 +361,8 @@ bool attn_tc_takes(const moe_attn_shape_t &s);
 int attn_tc_rows(const moe_attn_shape_t &s);
 cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, bool e4m3, int sms, bool chained, cudaStream_t st);
 
-// The decode kernel, one CTA of kDecodeWarps ranges per SM.
+// The decode kernel (head_dim 64 and 128), one CTA of kDecodeWarps ranges per SM.
 constexpr int kDecodeWarps = 8;
-bool attn_decode_takes(const moe_attn_shape_t &s);
 cudaError_t launch_attn_decode(const AttnParams &p, int head_dim, bool e4m3, int sms, cudaStream_t st);
 
 }  // namespace moe
