@@ -237,10 +237,12 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         prefetch_tmap(&tm_v);
     }
     tc_fence_before();
+    __shared__ Split<C::kThreads, 0, kBlk> s_split;          // wanted once more, at the end
     Split<C::kThreads, 0, kBlk> split;
     Cursor<0, kBlk> cur;
-    const long long n_blocks = split.init(p, cur, reinterpret_cast<long long *>(smem));           // has block barriers
+    const int n_blocks = static_cast<int>(split.init(p, cur, reinterpret_cast<long long *>(smem)));      // has block barriers
     tc_fence_after();
+    if (tid == 0) s_split = split;
     fence_async_smem();                                      // its shared memory is TMA's now
     __syncthreads();
     grid_dep_launch();
@@ -256,10 +258,10 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         return __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, &s_abort));
     };
     const int tile = p.tile_rows >> 1;                       // rows of a tile, at most 128
-    long long left = n_blocks;
-    // 16 warps x 128 registers at launch = 8 x 152 + 8 x 104: a softmax thread holds
+    int left = n_blocks;
+    // 16 warps x 128 registers at launch = 8 x 160 + 8 x 96: a softmax thread holds
     // 64 scores
-    if (kLoad != kLoadTma && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (kLoad != kLoadTma && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (kLoad == kLoadTma && warp == 10) {
         // ------------------------------------------------ K and V loads by TMA
         // lane: box of rows row .. row + box_rows - 1 of the block, columns 64 h ..
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
             // (like q), V fp16 (like p), both exactly.  A lane converts what it
             // copied itself.
             const uint32_t raw = ring + kSlots * C::kTile + first * kD + lane * 16;
-            long long todo = 2 * left;                       // K and V blocks to convert
+            int todo = 2 * left;                       // K and V blocks to convert
             int fill = 0;                                    // of the one to copy next, mod kDepth
             bool v_next = false;
             auto copy = [&]() {
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         };
         load_q(cur);
         while (left > 0 && ok) {
-            const int n = static_cast<int>(min(left, static_cast<long long>(cur.nblk - cur.blk)));
+            const int n = min(left, cur.nblk - cur.blk);
             Cursor<0, kBlk> nxt = cur;
             if (left > n) nxt.next_item(p);
             if (t * tile < cur.rows(p)) {
@@ -566,24 +568,22 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         }
     } else if (warp < 8) {
         // ------------------------------------------- softmax of tile t, a row each
-        if (kLoad != kLoadTma) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        if (kLoad != kLoadTma) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // lane 32 (warp mod 4) in bits 16..
         const uint32_t ts = tmem + C::kColS + 128 * t + lanes, to = tmem + C::kColO + 128 * t + lanes;
         const float mult = fmaxf(p.scale_log2, 1e-30f);                    // 0 times a masked -inf must stay -inf
         uint32_t ph = 0;                                     // of the barriers of the block's two halves
         bool ok = true, continued = cur.blk > 0;
-        long long item_from = 0;
+        int item_from = 0;
         while (left > 0 && ok) {
-            const int n = static_cast<int>(min(left, static_cast<long long>(cur.nblk - cur.blk)));
+            const int n = min(left, cur.nblk - cur.blk);
             const bool last = cur.blk + n == cur.nblk;
             const int rows = cur.rows(p);
             if (t * tile < rows) {
-                const int row = t * tile + r, grow = cur.row0(p) + row;
+                const int row = t * tile + r;
                 const bool real = r < tile && row < rows;
-                const long long tok = cur.r.qs + p.by_group.div(grow);
-                const int head = cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group);
-                const int lim = real ? row_limit(p, cur.r, grow) : 0;
+                const int lim = real ? row_limit(p, cur.r, cur.row0(p) + row) : 0;
                 float m = -INFINITY, l = 0.0f;               // m: largest q.k that O is relative to
                 for (int x = 0; x < 2 * n; ++x) {            // blocks of 64 keys
                     const int half = x & 1;
@@ -632,17 +632,19 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                     }
                     const float base = m == -INFINITY ? 0.0f : m * mult;
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    uint32_t w[32];
                     const float2 mult2 = make_float2(mult, mult), base2 = make_float2(-base, -base);
 #pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const float2 v = __ffma2_rn(make_float2(s[i], s[i + 1]), mult2, base2);
-                        const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                        sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
-                        w[i >> 1] = kLoad == kLoadCodes ? f16x2_of(e.x, e.y) : bf16x2_of(e.x, e.y);
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 v = __ffma2_rn(make_float2(s[c + i], s[c + i + 1]), mult2, base2);
+                            const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
+                            w[i >> 1] = kLoad == kLoadCodes ? f16x2_of(e.x, e.y) : bf16x2_of(e.x, e.y);
+                        }
+                        tmem_st16(ts + 64 * half + c / 2, w);
                     }
-                    tmem_st16(ts + 64 * half, w);
-                    tmem_st16(ts + 64 * half + 16, w + 16);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
@@ -655,7 +657,9 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                 tc_fence_after();
                 if (last && !continued) {
                     const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (tok * p.n_heads + head) * kD;
+                    const int grow = cur.row0(p) + row, tok = p.by_group.div(grow);
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                         (static_cast<long long>(cur.r.qs + tok) * p.n_heads + cur.kvh * p.group + (grow - tok * p.group)) * kD;
                     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll
                     for (int c = 0; c < kD; c += 32) {
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                     d.kvh = cur.kvh;
                     d.row0 = cur.row0(p);
                     d.rows = rows;
-                    if (!last && !continued) d.parts = split.parts(blockIdx.x, item_from, cur.nblk);
+                    if (!last && !continued) d.parts = s_split.parts(blockIdx.x, item_from, cur.nblk);
                     p.desc[blockIdx.x] = d;
                 }
             } else {
