@@ -135,6 +135,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         : "memory");
 }
 
+// The loads before it have landed.  The operands tie the values to it, so that
+// nothing computed from them moves before it.
+__device__ __forceinline__ void tmem_landed(float *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                   "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -593,10 +606,10 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                     float s[64];
                     tmem_ld32(ts + 64 * half, s);
                     tmem_ld32(ts + 64 * half + 32, s + 32);
-                    tmem_wait_ld();
+                    tmem_landed(s);
+                    tmem_landed(s + 32);
                     const int seen = lim - (cur.blk * kBlk + 64 * x);
-                    const bool masked = __any_sync(0xffffffffu, seen < 64);
-                    if (masked) {
+                    if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i) s[i] = i < seen ? s[i] : -INFINITY;
                     }
@@ -623,7 +636,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                             for (int c = 0; c < kD; c += 32) {
                                 float o[32];
                                 tmem_ld32(to + c, o);
-                                tmem_wait_ld();
+                                tmem_landed(o);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) o[i] *= f;
                                 tmem_st32(to + c, o);
@@ -665,7 +678,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                     for (int c = 0; c < kD; c += 32) {
                         float o[32];
                         tmem_ld32(to + c, o);
-                        tmem_wait_ld();
+                        tmem_landed(o);
                         if (real) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 16) {
@@ -682,7 +695,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                     for (int c = 0; c < kD; c += 32) {
                         float o[32];
                         tmem_ld32(to + c, o);
-                        tmem_wait_ld();
+                        tmem_landed(o);
                         if (real) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
