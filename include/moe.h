@@ -390,7 +390,7 @@ int moe_page_plan(const moe_page_shape_t *shape, const int32_t *cached, const in
  *               token's, multiples of 8 (0: adjacent); a fused projection's
  *               [tokens, n_heads + 2 n_kv_heads, head_dim] rows are read in place
  *   page_stride elements from page to page, a multiple of 16 (0: adjacent)
- *   k_scale, v_scale  static scales of an E4M3 cache (> 0; ignored for bf16)
+ *   k_scale, v_scale  static scales of an E4M3 cache (> 0, finite; ignored for bf16)
  */
 typedef struct {
     int32_t num_tokens, n_heads, n_kv_heads, head_dim, rot_dim, max_pos, interleaved;
@@ -425,7 +425,8 @@ int moe_rope_append(const moe_append_shape_t *shape, const void *q, const void *
 
 /*
  *   B           requests (1..4096)
- *   num_tokens  rows of q and out (>= 0; 0 is a no-op)
+ *   num_tokens  rows of q and out (>= 0; 0 is a no-op); num_tokens * n_heads is at
+ *               most 2^30
  *   n_heads, n_kv_heads  query heads and key/value heads (>= 1); n_heads is a
  *               multiple of n_kv_heads, and query head h reads key/value head
  *               h / (n_heads / n_kv_heads)
@@ -441,7 +442,7 @@ int moe_rope_append(const moe_append_shape_t *shape, const void *q, const void *
  *               of 8 (0: adjacent)
  *   page_stride elements from page to page, a multiple of 16 (0: adjacent)
  *   scale       multiplies q . k before the softmax
- *   k_scale, v_scale  static scales of an E4M3 cache (> 0; ignored for bf16)
+ *   k_scale, v_scale  static scales of an E4M3 cache (> 0, finite; ignored for bf16)
  */
 typedef struct {
     int32_t B, num_tokens, n_heads, n_kv_heads, head_dim;
@@ -459,7 +460,9 @@ int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes);
  * already, over the cache: for each new token t of request b and query head h
  *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
  * over the keys j the token sees.  Scores, the softmax's maximum and sum and
- * the accumulation are fp32; p enters its product with v rounded to 16 bits.
+ * the accumulation are fp32; p enters its product with v in 16 bits (bf16, fp16
+ *   with an E4M3 cache; as two bf16, a high and a low part, for requests with at
+ *   most 16 query rows a key/value head and head_dim up to 128).
  *   q [num_tokens, n_heads, head_dim] bf16 (16-byte aligned), k_cache, v_cache
  *   (16-byte aligned), block_table [B, max_pages], q_start [B+1], kv_len [B] in;
  *   out [num_tokens, n_heads, head_dim] bf16 (16-byte aligned) out.

@@ -826,8 +826,12 @@ static int check_attn(const moe_attn_shape_t *shape)
     if (s.q_stride && (s.q_stride < static_cast<int64_t>(s.n_heads) * s.head_dim || s.q_stride % 8)) return MOE_ERR_INVALID_ARG;
     if (s.page_stride && (s.page_stride < static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim || s.page_stride % 16))
         return MOE_ERR_INVALID_ARG;
-    if (!(s.scale - s.scale == 0.0f)) return MOE_ERR_INVALID_ARG;          // not finite
-    if (s.cache_dtype == MOE_E4M3 && (!(s.k_scale > 0.0f) || !(s.v_scale > 0.0f))) return MOE_ERR_INVALID_ARG;
+    // no address computed from a stride may leave 63 bits
+    if (s.q_stride > (1ll << 60) / (s.num_tokens + 1ll) || s.page_stride > (1ll << 60) / s.num_pages) return MOE_ERR_INVALID_ARG;
+    auto finite = [](float x) { return x - x == 0.0f; };
+    if (!finite(s.scale)) return MOE_ERR_INVALID_ARG;
+    if (s.cache_dtype == MOE_E4M3 && !(s.k_scale > 0.0f && s.v_scale > 0.0f && finite(s.k_scale) && finite(s.v_scale)))
+        return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -220,7 +220,12 @@ extern "C" int moe_rope_append(const moe_append_shape_t *shape, const void *q, c
     if (p.qs < q_row || p.ks < kv_row || p.vs < kv_row || p.page_stride < kv_row * s.page_size || p.qs % 8 || p.ks % 8 ||
         p.vs % 8 || p.page_stride % 16)
         return MOE_ERR_INVALID_ARG;
-    if (s.cache_dtype == MOE_E4M3 && (!(s.k_scale > 0.0f) || !(s.v_scale > 0.0f))) return MOE_ERR_INVALID_ARG;
+    // no address computed from a stride may leave 63 bits
+    const int64_t most = (1ll << 60) / (s.num_tokens + 1ll);
+    if (p.qs > most || p.ks > most || p.vs > most || p.page_stride > (1ll << 60) / s.num_pages) return MOE_ERR_INVALID_ARG;
+    auto finite = [](float x) { return x - x == 0.0f; };
+    if (s.cache_dtype == MOE_E4M3 && !(s.k_scale > 0.0f && s.v_scale > 0.0f && finite(s.k_scale) && finite(s.v_scale)))
+        return MOE_ERR_INVALID_ARG;
     if (s.num_tokens == 0) return MOE_OK;
     if (!q || !k || !v || !slots || !q_out || !k_cache || !v_cache) return MOE_ERR_INVALID_ARG;
     if (s.rot_dim > 0 && (!positions || !cos_sin)) return MOE_ERR_INVALID_ARG;

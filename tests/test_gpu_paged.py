@@ -189,6 +189,31 @@ def test_append_is_undone_by_the_inverse_step():
     assert ((back - q).abs() <= ref.U_E4M3 * q.abs() + size * (1.5 * 2 ** -8 * (1 + ref.U_E4M3) + 2 ** -10 / 448 * 1.1)).all()
 
 
+@pytest.mark.parametrize("scale", [1 / 64, 0.017, 3.3e-4, 1.0, 700.0, 1e-20, 1e-30, 3e25])
+def test_append_codes_are_those_of_the_ieee_quotient(scale):
+    """v's codes bit for bit (no rotation in the way), with zeros of both signs,
+    subnormals, midpoints of codes, saturating and non-finite values, and scales on
+    both sides of the range in which the quotient is formed from the reciprocal."""
+    g = torch.Generator().manual_seed(1)
+    T, G, D = 400, 2, 64
+    x = torch.randn(T, G, D, generator=g, dtype=torch.float64) * 10.0 ** (torch.rand(T, G, D, generator=g, dtype=torch.float64) * 7 - 4)
+    x[0] = torch.linspace(-30, 30, G * D).reshape(G, D)
+    v = (x * scale).to(torch.bfloat16)
+    v[1, 0, :8] = torch.tensor([0.0, -0.0, float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 1e-40]).to(torch.bfloat16)
+    q = torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    s = moe.AppendShape(num_tokens=T, n_heads=1, n_kv_heads=G, head_dim=D, page_size=16, num_pages=T // 16, cache_dtype=moe.E4M3,
+                        k_scale=scale, v_scale=scale)
+    kc, vc = (torch.zeros(T // 16, 16, G, D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    dv = v.cuda()
+    moe.rope_append(s, q, dv, dv, None, torch.arange(T, dtype=torch.int32, device="cuda"), None, q.clone(), kc, vc)
+    want = (v.float() / torch.tensor(scale, dtype=torch.float32)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for c in (kc, vc):
+        got = c.cpu().reshape(T, G, D)
+        nan = v.isnan()
+        assert ((got & 0x7F) == 0x7F)[nan].all()
+        assert torch.equal(got[~nan], want[~nan])
+
+
 def test_append_flags_bad_slots_and_positions():
     T, D = 6, 64
     x = torch.randn(T, 3, D).to(torch.bfloat16).cuda()
@@ -387,17 +412,65 @@ def test_attention_same_bits_every_time_on_streams_and_in_graphs():
     assert ((d.out.cpu().double() - want).abs() <= tol).all()
 
 
-def test_attention_offsets_beyond_32_bits():
-    """Pages whose elements lie more than 2^31 (and bytes more than 2^32) into the
-    cache."""
-    ps, g, dim = 64, 8, 128
-    pages = 2 ** 31 // (ps * g * dim) + 40
-    k_cache = torch.zeros(pages, ps, g, dim, dtype=torch.bfloat16, device="cuda")
-    b = ref.Batch([1, 40], [100, 130], heads=16, kv_heads=g, dim=dim, ps=ps, seed=9)
+def test_attention_two_calls_at_once():
+    """Two streams, a workspace each: the bits of either call alone."""
+    batches = [ref.Batch([1] * 40, [50 * i + 7 for i in range(40)], heads=8, kv_heads=2, dim=128, seed=12),
+               ref.Batch([300, 1, 128], [900, 1500, 1000], heads=8, kv_heads=2, dim=128, seed=13)]
+    ds = [Dev(b) for b in batches]
+    alone = [d.run().clone() for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for d, st in zip(ds, streams):
+            with torch.cuda.stream(st):
+                d.out.fill_(7)
+                d.run()
+    torch.cuda.synchronize()
+    for d, want in zip(ds, alone):
+        assert torch.equal(d.out, want)
+
+
+@pytest.mark.parametrize("B,q_most,kv_most,kw", [(700, 3, 90, dict(heads=4, kv_heads=2, dim=64)), (4096, 1, 9, dict(heads=2, kv_heads=1, dim=64)),
+                                                 (150, 40, 90, dict(heads=4, kv_heads=1, dim=64, e4m3=True, ps=24)),
+                                                 (333, 1, 400, dict(heads=4, kv_heads=4, dim=128, e4m3=True))])
+def test_attention_many_requests(B, q_most, kv_most, kw):
+    r = np.random.default_rng(B)
+    q = r.integers(0, q_most + 1, B)
+    q[:70] = 0                                           # a run of requests without tokens
+    kv = np.maximum(q, r.integers(0, kv_most + 1, B))
+    _check_attn(ref.Batch(q.tolist(), kv.tolist(), seed=B, **kw))
+
+
+def test_attention_without_any_token_writes_nothing():
+    for max_q in (0, 1):
+        d = Dev(ref.Batch([0, 0], [5, 0], heads=4, kv_heads=2, dim=64, pad_rows=3), max_q)
+        assert (d.run() == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_output_aligned_to_16_bytes_only(dim):
+    b = ref.Batch([70, 1], [200, 90], heads=4, kv_heads=2, dim=dim, seed=14)
     d = Dev(b)
+    n = b.T * b.heads * dim
+    d.out = torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")[8:8 + n].view(b.T, b.heads, dim)
+    assert d.out.data_ptr() % 32 == 16
+    out = d.run().cpu().double()
+    want, tol = b.reference()
+    assert ((out - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3,ps", [(False, 64), (False, 24), (True, 64)])
+def test_attention_offsets_beyond_32_bits(e4m3, ps):
+    """Pages whose elements lie more than 2^31 (and bytes more than 2^32) into the
+    cache, for single tokens and for chunks."""
+    g, dim = 8, 128
+    pages = (2 if e4m3 else 1) * 2 ** 31 // (ps * g * dim) + 40
+    b = ref.Batch([1, 40], [100, 130], heads=16, kv_heads=g, dim=dim, ps=ps, seed=9, e4m3=e4m3)
+    d = Dev(b)
+    k_cache = torch.zeros(pages, ps, g, dim, dtype=d.k_cache.dtype, device="cuda")
     shift = pages - b.num_pages
     k_cache[shift:].copy_(d.k_cache)
-    k_cache[:shift].fill_(float("nan"))
+    k_cache[:shift].fill_(0x7F if e4m3 else float("nan"))
     v_cache = k_cache.clone()
     v_cache[shift:].copy_(d.v_cache)
     d.k_cache, d.v_cache = k_cache, v_cache

@@ -59,7 +59,8 @@ def _append(**kw):
     (dict(head_dim=96, rot_dim=96), -2), (dict(q_stride=1016), -1), (dict(q_stride=1028), -1), (dict(k_stride=128), -1),
     (dict(v_stride=260), -1), (dict(page_stride=4088), -1), (dict(page_stride=4104), -1),
     (dict(cache_dtype=1, k_scale=0.0), -1), (dict(cache_dtype=1, v_scale=-1.0), -1),
-    (dict(cache_dtype=1, v_scale=math.nan), -1), (dict(num_pages=1 << 27), -1), (dict(num_tokens=0), 0)])
+    (dict(cache_dtype=1, v_scale=math.nan), -1), (dict(cache_dtype=1, k_scale=math.inf), -1), (dict(num_pages=1 << 27), -1),
+    (dict(q_stride=1 << 62), -1), (dict(page_stride=1 << 62), -1), (dict(num_tokens=0), 0)])
 def test_rope_append_checks_shapes(lib, kw, code):
     ptr = None if code == 0 else A
     assert lib.moe_rope_append(C.byref(_append(**kw)), ptr, A, A, A, A, A, 2 * A, A, A, None, None) == code
@@ -93,6 +94,7 @@ BAD_ATTN = [
     (dict(q_stride=1000), -1), (dict(q_stride=1028), -1), (dict(page_stride=4088), -1), (dict(page_stride=4104), -1),
     (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(cache_dtype=1, k_scale=0.0), -1),
     (dict(cache_dtype=1, v_scale=math.nan), -1), (dict(num_pages=1 << 27), -1), (dict(max_pages=1 << 27), -1),
+    (dict(cache_dtype=1, k_scale=math.inf), -1), (dict(q_stride=1 << 62), -1), (dict(page_stride=1 << 62), -1),
     (dict(num_tokens=1 << 29), -1)]
 
 
