@@ -1,43 +1,26 @@
 // paged_attention.cu - attention of a batch's new tokens over a paged cache
-// (moe_paged_attention): the kernel for few query rows per request and for
-// every layout the tensor-memory kernel does not take, the kernel that joins
-// partial results, and the entry point.
+// (moe_paged_attention): the entry point with its choice of kernels, the kernel
+// that joins partial results, and the kernel for the shapes the other two do not
+// take.
 //
 // o_i = sum_j p_ij v_j / sum_j p_ij with p_ij = 2^(s_ij - m_i), s = q.k scale
 // log2(e), in one pass over the keys with the running maximum m_i and sum: when
 // a block of keys raises m_i, what was summed so far is scaled by 2^(old - new).
 //
-// A decode step reads every key and value of its requests once and does 4 group
-// operations per element read, so HBM bounds it: at 64 requests of up to 8192
-// keys 1.08 GB.  What it takes is bytes in flight from the first moment to the
-// last on every SM (see paged_work.cuh for the division of the work): a ring of
-// kStages blocks of 64 keys filled by cp.async, 2 to 3 CTAs per SM, and a load
-// side that runs ahead of the compute side over the borders of items, so that
-// short sequences keep the ring full too.  Page ids are read two blocks ahead
-// and turned into row offsets one block ahead.
-//
-// Products run on mma.sync m16n8k16: the 16 rows of one are the query heads of
-// a group, which tcgen05's 128 rows would leave nearly empty, and at this
-// arithmetic intensity the tensor pipe idles either way.
+// Requests with at most 16 query rows a key/value head are bound by reading the
+// cache and go to paged_decode.cu, those with more by the products and exponentials
+// and go to paged_attention_tc.cu.  The kernel here takes head_dim 256 (for both:
+// kWM = 1 and 4), whose accumulators leave the others no room, and with many rows a
+// negative scale or a group of more than 128 heads.  It is mma.sync with 64-key
+// blocks in a ring that all four warps fill by cp.async and read behind a block
+// barrier; the warps lie down the rows, or with few rows along the keys of a block.
+// 130 to 160 TFLOP/s on prompts at head_dim 128.
 #include <atomic>
 
 #include "paged_mma.cuh"
 #include "paged_work.cuh"
 
 namespace moe {
-
-__device__ __forceinline__ uint32_t attn_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Geometry of one kernel: kWM warps down the query rows (16 each), 4 / kWM
 // along the keys of a block.
@@ -69,7 +52,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
     __shared__ long long s_off[2][kBlk];         // element offset of each key's row, -1: none
     __shared__ float s_inv[kRows];               // 1 / the row's factor in q (E4M3 cache)
     __shared__ float s_m[4][16], s_l[4][16];
-    const uint32_t ring = attn_smem(smem);
+    const uint32_t ring = smem_u32(smem);
     uint8_t *s_q = smem + kStages * C::kStage;
     float *s_merge = reinterpret_cast<float *>(s_q + C::kQ);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -123,8 +106,8 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             const long long off = s_off[buf][r];
             const long long at = (off < 0 ? 0 : off * esz) + c * 16;
             const uint32_t d = dst + r * kRowBytes + chunk_of<kChunks>(r, c) * 16;
-            cp_async16(d, static_cast<const uint8_t *>(p.k_cache) + at, off >= 0);
-            cp_async16(d + kBlk * kRowBytes, static_cast<const uint8_t *>(p.v_cache) + at, off >= 0);
+            copy16(d, static_cast<const uint8_t *>(p.k_cache) + at, off >= 0);
+            copy16(d + kBlk * kRowBytes, static_cast<const uint8_t *>(p.v_cache) + at, off >= 0);
         }
     };
 
@@ -137,7 +120,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {      // block i's offsets are in buffer i & 1
         if (i < n_blocks) issue(i, i & 1);
-        cp_async_commit();
+        copies_commit();
         if (warp < 2) {
             put_off((i + 1) & 1);
             read_id();
@@ -155,14 +138,14 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
     bool fresh_item = true;
     long long item_from = 0;                     // where in this CTA's range the item starts
     bool continued = cur.blk > 0;
-    const uint32_t sq = attn_smem(s_q);
+    const uint32_t sq = smem_u32(s_q);
     auto load_qf = [&](uint32_t (&f)[4], int ks) {
         const int r = 16 * wm + (lane & 15), c = 2 * ks + (lane >> 4);
         ldsm4(f, sq + r * (kD * 2) + (c ^ (r & 7)) * 16);
     };
 
     for (long long it = 0; it < n_blocks; ++it) {
-        cp_async_wait<kStages - 2>();
+        copies_wait<kStages - 2>();
         if (fresh_item) {
             // the item's query rows into shared memory; for an E4M3 cache in fp16
             // (see row_power), the columns permuted within 16 to the order in
@@ -219,7 +202,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
         {
             const long long nx = it + kStages - 1;
             if (nx < n_blocks) issue(static_cast<int>(nx % kStages), static_cast<int>(nx & 1));
-            cp_async_commit();
+            copies_commit();
             if (warp < 2) {
                 put_off(static_cast<int>((nx + 1) & 1));
                 read_id();
@@ -494,7 +477,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             ++cur.blk;
         }
     }
-    cp_async_wait<0>();
+    copies_wait<0>();
     if (bad && p.status) set_status(p.status, MOE_ERR_DEVICE_CHECK);
     if (p.wait_at_end) grid_dep_wait();
 }

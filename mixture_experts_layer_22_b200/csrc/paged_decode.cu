@@ -26,17 +26,6 @@
 
 namespace moe {
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int kD, bool kE4m3>
 struct DecCfg {
     static constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps;

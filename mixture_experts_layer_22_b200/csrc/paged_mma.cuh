@@ -1,5 +1,5 @@
-// paged_mma.cuh - the mma.sync pieces that the paged-attention kernels for few
-// query rows share.
+// paged_mma.cuh - pieces that the paged-attention kernels share: copies into shared
+// memory, mma.sync with its operand loads, conversions.
 #pragma once
 #include <cstdint>
 
@@ -7,6 +7,20 @@
 #include <cuda_fp16.h>
 
 namespace moe {
+
+// 16 bytes to shared memory without passing through registers, zeros if !valid
+// (the source address is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
 {
