@@ -11,7 +11,7 @@
 // cache and go to paged_decode.cu, those with more by the products and exponentials
 // and go to paged_attention_tc.cu.  The kernel here takes head_dim 256 (for both:
 // kWM = 1 and 4), whose accumulators leave the others no room, and with many rows a
-// negative scale or a group of more than 128 heads.  It is mma.sync with 64-key
+// scale that is zero or negative or a group of more than 128 heads.  It is mma.sync with 64-key
 // blocks in a ring that all four warps fill by cp.async and read behind a block
 // barrier; the warps lie down the rows, or with few rows along the keys of a block.
 // 130 to 160 TFLOP/s on prompts at head_dim 128.
@@ -868,9 +868,8 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     p.num_pages = s.num_pages;
     p.max_pages = s.max_pages;
     p.causal = s.causal;
-    const bool e4m3 = s.cache_dtype == MOE_E4M3;
-    p.scale_log2 = s.scale * (e4m3 ? s.k_scale : 1.0f) * 1.4426950408889634f;
-    p.v_scale = e4m3 ? s.v_scale : 1.0f;
+    p.scale_log2 = attn_scale_log2(s);
+    p.v_scale = s.cache_dtype == MOE_E4M3 ? s.v_scale : 1.0f;
     cudaStream_t sm = reinterpret_cast<cudaStream_t>(stream);
     char *wb = static_cast<char *>(ws);
     if (s.head_dim == 64) return launch_attention<64>(s, p, wb, sm, launches);

@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // lane 32 (warp mod 4) in bits 16..
         const uint32_t ts = tmem + C::kColS + 128 * t + lanes, to = tmem + C::kColO + 128 * t + lanes;
-        const float mult = fmaxf(p.scale_log2, 1e-30f);                    // 0 times a masked -inf must stay -inf
+        const float mult = p.scale_log2;                                   // > 0: a masked -inf stays one
         uint32_t ph = 0;                                     // of the barriers of the block's two halves
         bool ok = true, continued = cur.blk > 0;
         int item_from = 0;
@@ -796,10 +796,11 @@ static bool query_map(CUtensorMap *m, const AttnParams &p, int kD)
 
 bool attn_tc_takes(const moe_attn_shape_t &s)
 {
-    // a tile of 128 rows holds whole tokens, and the maximum of q.k is that of the
-    // scores; the query map's stride is below 2^40 bytes
+    // a tile of 128 rows holds whole tokens, the maximum of q.k is that of the scores
+    // (and times the scale still -inf where it is); the query map's stride is below
+    // 2^40 bytes
     if (s.head_dim != 64 && s.head_dim != 128) return false;
-    return s.n_heads / s.n_kv_heads <= 128 && s.scale >= 0.0f && s.q_stride < 1ll << 39;
+    return s.n_heads / s.n_kv_heads <= 128 && attn_scale_log2(s) >= 1e-37f && s.q_stride < 1ll << 39;
 }
 
 int attn_tc_rows(const moe_attn_shape_t &s)

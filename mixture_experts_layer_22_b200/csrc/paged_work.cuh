@@ -355,6 +355,12 @@ struct Split {
     }
 };
 
+// What q.k, or q times a code, is multiplied by to be an exponent of 2.
+inline float attn_scale_log2(const moe_attn_shape_t &s)
+{
+    return s.scale * (s.cache_dtype == MOE_E4M3 ? s.k_scale : 1.0f) * 1.4426950408889634f;
+}
+
 // The tensor-memory kernel: whether it takes a shape, the query rows of its items,
 // its launch with one CTA (and range) per SM.
 bool attn_tc_takes(const moe_attn_shape_t &s);

@@ -441,6 +441,21 @@ def test_attention_many_requests(B, q_most, kv_most, kw):
     _check_attn(ref.Batch(q.tolist(), kv.tolist(), seed=B, **kw))
 
 
+@pytest.mark.parametrize("kw", [dict(ps=16), dict(ps=24), dict(ps=128, e4m3=True), dict(ps=64, causal=False), dict(ps=40, causal=False),
+                                dict(ps=7, causal=False, e4m3=True)], ids=str)
+def test_attention_many_items_of_many_rows(kw):
+    """Several items a CTA, rings that go round many times, ranges that begin and end
+    inside items, last tiles of one row."""
+    _check_attn(ref.Batch([1025, 700, 1281], [1025, 1500, 1300], heads=16, kv_heads=16, dim=64, seed=15, **kw))
+
+
+@pytest.mark.parametrize("spread,scale", [(1e17, 1e-34), (3e18, 3e-38), (1.0, 1e-42)])
+def test_attention_tiny_scales(spread, scale):
+    """Scores of ordinary size from a tiny scale and large queries."""
+    for kw in ({}, dict(e4m3=True)):
+        _check_attn(ref.Batch([40, 1], [90, 50], heads=4, kv_heads=2, dim=64, seed=16, spread=spread, scale=scale, **kw))
+
+
 def test_attention_without_any_token_writes_nothing():
     for max_q in (0, 1):
         d = Dev(ref.Batch([0, 0], [5, 0], heads=4, kv_heads=2, dim=64, pad_rows=3), max_q)
