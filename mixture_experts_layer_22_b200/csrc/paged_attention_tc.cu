@@ -477,16 +477,14 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
             }
             return x;
         };
-        auto scores = [&](int kslot, int half) {             // S half = Q K[64 half ..]^T
-            if (elect_one()) {
-                const uint32_t b = ring + kslot * C::kTile + half * 8192;
+        auto scores = [&](int kslot, int half) {             // S half = Q K[64 half ..]^T, by the elected lane
+            const uint32_t b = ring + kslot * C::kTile + half * 8192;
 #pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    const uint32_t at = (ks >> 2) * C::kHalf + (ks & 3) * 32;
-                    mma_bf16(ts + 64 * half, sdesc_k_sw128(q0 + at), sdesc_k_sw128(b + at), idesc_s, ks > 0);
-                }
-                mma_commit(smem_u32(&s_sfull[t][half]));
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const uint32_t at = (ks >> 2) * C::kHalf + (ks & 3) * 32;
+                mma_bf16(ts + 64 * half, sdesc_k_sw128(q0 + at), sdesc_k_sw128(b + at), idesc_s, ks > 0);
             }
+            mma_commit(smem_u32(&s_sfull[t][half]));
         };
         uint32_t q_under_way = 0;
         const uint64_t policy = policy_evict_normal();
@@ -515,9 +513,11 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                 qphase ^= 1u;
                 q_under_way = 0;
                 tc_fence_after();
-                scores(kslot, 0);
-                scores(kslot, 1);
-                if (elect_one()) mma_commit(smem_u32(&s_empty[kslot]));
+                if (elect_one()) {
+                    scores(kslot, 0);
+                    scores(kslot, 1);
+                    mma_commit(smem_u32(&s_empty[kslot]));
+                }
                 for (int j = 0; j < n && ok; ++j) {
                     const int vslot = next_fill();
                     if (!ok) break;
@@ -534,31 +534,35 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                     }
+                    if (j + 1 < n) {
+                        kslot = next_fill();
+                        if (!ok) break;
+                    }
+                    // From P's arrival to the next scores' is what a tile waits for, so
+                    // nothing stands between: the product, the scores behind it in the
+                    // half's columns, and only then who else is told.
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         ok = wait(&s_pfull[t][half], pphase);
                         if (!ok) break;
                         tc_fence_after();
-                        // the item's last scores are done: its Q may go
-                        if (half == 1 && j + 1 == n && left > n) load_q(nxt);
                         if (elect_one()) {
                             const uint32_t b = ring + vslot * C::kTile + half * 8192;
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ta(to, ts + 64 * half + 8 * ks, sdesc_mn_sw128(b + ks * 2048, C::kHalf), idesc_o,
                                            j > 0 || half > 0 || ks > 0);
+                            if (j + 1 < n) scores(kslot, half);
                             mma_commit(smem_u32(&s_pv[t][half]));
-                            if (half == 1) mma_commit(smem_u32(&s_empty[vslot]));
-                        }
-                        if (j + 1 < n) {
-                            if (half == 0) {
-                                kslot = next_fill();
-                                if (!ok) break;
+                            if (half == 1) {
+                                mma_commit(smem_u32(&s_empty[vslot]));
+                                if (j + 1 < n) mma_commit(smem_u32(&s_empty[kslot]));
                             }
-                            scores(kslot, half);
-                            if (half == 1 && elect_one()) mma_commit(smem_u32(&s_empty[kslot]));
                         }
+                        __syncwarp();
                     }
+                    // the item's last scores are done: its Q may go
+                    if (ok && j + 1 == n && left > n) load_q(nxt);
                     pphase ^= 1u;
                 }
             } else {
