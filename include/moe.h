@@ -333,8 +333,9 @@ int moe_inv_rope_quant_per_head(const moe_rope_shape_t *shape, const void *x, co
  *     (if it was 0) when a kernel finds bad data, and left unchanged
  *     otherwise.  No value in a device array makes a kernel access memory
  *     outside the buffers described here.
- *   - Two calls in flight at once may share inputs, but not outputs or a
- *     workspace.
+ *   - Outputs and the workspace overlap neither the inputs nor one another,
+ *     except where it is said below.  Two calls in flight at once may share
+ *     inputs, but not outputs or a workspace.
  */
 
 /*
@@ -362,8 +363,8 @@ typedef struct {
  *     positions [max_tokens]  cached[b] + i of request b's i-th new token
  *     slots     [max_tokens]  that position's cache slot
  *     free_next [1]           *free_pos + pages taken
- *   Padding rows get position 0 and slot -1.  free_next may be NULL and must
- *   not be free_pos.
+ *   Padding rows get position 0 and slot -1.  free_next may be NULL.  An output
+ *   that overlaps an input (kv_len on cached, free_next on free_pos) is refused.
  *   Bad data sets the status, and: a request with a negative length or with
  *   cached + fresh > max_pages * page_size counts as cached = fresh = 0; a page
  *   that cannot be had (the free list has run out, or its id is outside

@@ -846,6 +846,7 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
         (reinterpret_cast<uintptr_t>(ws) & 255))
         return MOE_ERR_INVALID_ARG;
     if (ws_bytes < attn_ws(s).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (out == q) return MOE_ERR_INVALID_ARG;
     AttnParams p;
     p.q = q;
     p.k_cache = k_cache;

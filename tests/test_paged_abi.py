@@ -45,6 +45,21 @@ def test_page_plan_cursor_must_not_be_its_own_successor(lib):
     assert lib.moe_page_plan(C.byref(_page()), A, A, A, A, A, A, A, A, A, A, None, None) == -1
 
 
+# cached, fresh, free_pages, free_pos, block_table, q_start, kv_len, positions, slots, free_next, each at
+# its own address (nothing here reaches a launch)
+APART = [A * (1 << i) for i in range(10)]
+
+
+@pytest.mark.parametrize("out", [4, 5, 6, 7, 8, 9])
+@pytest.mark.parametrize("into", [0, 1, 2, 3])
+def test_page_plan_outputs_must_not_overlap_inputs(lib, out, into):
+    words = dict(zip(range(10), (4, 4, 10, 1, 32, 5, 4, 16, 16, 1)))
+    for at in (APART[into], APART[into] + 4 * (words[into] - 1), APART[into] - 4 * (words[out] - 1)):
+        args = list(APART)
+        args[out] = at
+        assert lib.moe_page_plan(C.byref(_page()), *args, None, None) == -1
+
+
 def _append(**kw):
     base = dict(num_tokens=8, n_heads=8, n_kv_heads=2, head_dim=128, rot_dim=128, max_pos=64, interleaved=0, page_size=16,
                 num_pages=64, cache_dtype=0, k_scale=1.0, v_scale=1.0)
@@ -121,6 +136,11 @@ def test_paged_attention_rejects_null_misaligned_and_small(lib):
     assert lib.moe_paged_attention(C.byref(s), *good, need - 1, None) == -3
     assert lib.moe_attn_workspace_size(C.byref(s), None) == -1
     assert lib.moe_paged_attention(C.byref(_attn(num_tokens=0)), *([None] * 9), 0, None) == 0
+
+
+def test_paged_attention_output_is_not_q(lib):
+    s = _attn()
+    assert lib.moe_paged_attention(C.byref(s), A, A, A, A, A, A, A, None, A, moe.attn_workspace_size(s), None) == -1
 
 
 def test_reference_attention_against_torch():
