@@ -289,11 +289,12 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
             const float alpha = exp2_fast(m[h] - base);
             m[h] = mn;
             l[h] *= alpha;
+            const float from = kE4m3 ? base - kF16Up : base;
 #pragma unroll
             for (int i = 0; i < kKeys / 8; ++i)
 #pragma unroll
                 for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                    s[i][e] = exp2_fast(s[i][e] - base);
+                    s[i][e] = exp2_fast(s[i][e] - from);
                     l[h] += s[i][e];
                 }
             if (alpha != 1.0f) {

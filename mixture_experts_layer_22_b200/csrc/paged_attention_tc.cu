@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                             }
                         }
                     }
-                    const float base = m == -INFINITY ? 0.0f : m * mult;
+                    const float base = m == -INFINITY ? 0.0f : kLoad == kLoadCodes ? __fmaf_rn(m, mult, -kF16UpLag) : m * mult;
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     const float2 mult2 = make_float2(mult, mult), base2 = make_float2(-base, -base);
 #pragma unroll

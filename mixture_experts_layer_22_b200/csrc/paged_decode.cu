@@ -234,11 +234,12 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
                 alpha[h] = exp2_fast(m[h] - base);
                 m[h] = top;
                 l[h] *= alpha[h];
+                const float from = kE4m3 ? base - kF16Up : base;
 #pragma unroll
                 for (int i = 0; i < kBlk / 8; ++i)
 #pragma unroll
                     for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                        s[i][e] = exp2_fast(s[i][e] - base);
+                        s[i][e] = exp2_fast(s[i][e] - from);
                         l[h] += s[i][e];
                     }
             }

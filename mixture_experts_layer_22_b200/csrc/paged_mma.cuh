@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b)
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// With a cache of codes p enters its product as fp16, whose smallest step is 2^-24.
+// It is formed times 2^15 (its largest is 1) or 2^7 (2^8 where the maximum it is
+// relative to may lag behind), and so is the sum of a row: the factor leaves with the
+// quotient, and a weight may be 2^-32 of the largest before it is lost.  Plain, a
+// quarter of a million keys of 2^-26 each, 2^-8 together, were.
+constexpr float kF16Up = 15.0f, kF16UpLag = 7.0f;
+
 __device__ __forceinline__ uint32_t f16x2_of(float a, float b)
 {
     const __half2 r = __floats2half2_rn(a, b);

@@ -70,8 +70,9 @@ def attention(q, k, v, q_lens, kv_lens, causal, scale, u_p):
     q [T, H, D]; k, v: per request [kv, G, D]; all float64.  The bound per
     element, with A = sum_j p_j |v_j| (so |out| <= A):
       out's own rounding            U_BF16 |out|
-      p's rounding before p v       u_p A (p in 16 bits; for fp16 p also half its
-                                    smallest step, 2^-25, per key)
+      p's rounding before p v       u_p A (p in 16 bits; for fp16 p, formed times
+                                    2^7 at least, also half its smallest step,
+                                    2^-32, per key)
       scores: D products and sums in fp32, the scale and the exponent's argument
       (|s| log2 e large) rounded: an error e_s in s changes p by e_s p, in
       numerator and denominator    2 e_s A
@@ -98,7 +99,7 @@ def attention(q, k, v, q_lens, kv_lens, causal, scale, u_p):
             e_s = (mag.amax(-1, keepdim=True) if kv else torch.zeros(n, 1)) * (D + 8) * U_F32
             vmax = vv.abs().max() if kv else 0.0
             tol[at:at + n, h] = (U_BF16 * (p @ vv).abs() + A * (u_p + 2 * e_s + 2 * (2.0 ** -22 + (kv + 64) * U_F32)) +
-                                 (kv * 2.0 ** -25 * vmax if u_p == U_F16 else 0.0) + 2.0 ** -130)
+                                 (kv * 2.0 ** -32 * vmax if u_p == U_F16 else 0.0) + 2.0 ** -130)
         at += n
     return out, tol
 

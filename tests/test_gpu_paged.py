@@ -1,5 +1,7 @@
 """GPU tests of the paged-attention operators against 64-bit forms of their
 definitions."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -494,6 +496,35 @@ def test_attention_offsets_beyond_32_bits(e4m3, ps):
     out = d.run().cpu().double()
     want, tol = b.reference()
     assert int(d.status[0]) == 0 and ((out - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,n,heads", [(64, 1, 1), (128, 1, 4), (256, 1, 1), (64, 40, 1), (128, 40, 2), (256, 40, 1)])
+@pytest.mark.parametrize("at", [0, 100000])
+def test_attention_many_small_weights_beside_a_large_one(e4m3, dim, n, heads, at):
+    """One key with weight 1 and value 0, a quarter of a million with weight 2^-26
+    and value 1: less than 16 bits' smallest steps each, 2^-8 together.  Requests
+    enough (of the same pages) that one range of keys holds a whole one."""
+    kv, ps, B = 2 ** 18, 1024, 1400 if n == 1 else 400 if dim == 256 else 170
+    one = 0x38 if e4m3 else 1.0
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    k = torch.zeros(kv // ps, ps, 1, dim, dtype=dt, device="cuda")
+    v = torch.full_like(k, one)
+    k[at // ps, at % ps], v[at // ps, at % ps] = one, 0
+    q = torch.ones(B * n, heads, dim, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    s = moe.AttnShape(B=B, num_tokens=B * n, n_heads=heads, n_kv_heads=1, head_dim=dim, page_size=ps, num_pages=kv // ps,
+                      max_pages=kv // ps, causal=1, max_q=n, cache_dtype=int(e4m3), scale=26 * math.log(2) / dim, k_scale=1.0,
+                      v_scale=1.0)
+    table = torch.arange(kv // ps, dtype=torch.int32, device="cuda").repeat(B, 1)
+    moe.paged_attention(s, q, k, v, table, _i32(range(0, B * n + 1, n)), _i32([kv] * B), out, moe.attn_workspace(s))
+    small = 2.0 ** -26 * (kv - n + torch.arange(n, dtype=torch.float64)[:, None, None])
+    want = small / (1 + small)
+    # out's rounding; p's, and up to 2^-32 a key; the score of 26 rounded dim + 8 times, in both sums; ex2's
+    # 2^-22 and the sums of kv terms
+    tol = want * (ref.U_BF16 + ref.U_BF16 + 2.0 ** -32 / 2.0 ** -26 + 2 * 26 * math.log(2) * (dim + 8) * ref.U_F32 +
+                  2 * (2.0 ** -22 + (kv + 64) * ref.U_F32))
+    assert ((out.cpu().double().reshape(B, n, heads, dim) - want).abs() <= tol).all()
 
 
 def test_binding_refuses_wrong_tensors():
