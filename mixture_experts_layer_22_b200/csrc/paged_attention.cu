@@ -760,11 +760,20 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         p.by_tile.set(rows);
     };
     items_of(kFewRows);
+    p.team_log = 0;
     int r;
     if constexpr (kD <= 128) {
+        // Heads side by side until a team reads 256 bytes of a key.  Rows of 64 bytes
+        // alone had every 128-byte line fetched twice (128 requests, E4M3, D = 64: 165 to
+        // 110 us; D = 128: 208 to 183; bf16, D = 64: 104 to 97).  Teams of 512 and
+        // 1024 bytes: 115, 181, 96 and 115, 186, 99, and slower with few keys.
+        const int row_bytes = kD * (e4m3 ? 1 : 2);
+        while (s.n_kv_heads % (2 << p.team_log) == 0 && row_bytes << p.team_log < 256) ++p.team_log;
+        p.n_teams = s.n_kv_heads >> p.team_log;
         few = AttnParts{p.part, p.desc, sms * kDecodeWarps, kFewRows};
         if (launch_attn_decode(p, kD, e4m3, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
     } else {
+        p.n_teams = s.n_kv_heads;
         r = e4m3 ? launch_mma<kD, true, 1>(p, few, false, st) : launch_mma<kD, false, 1>(p, few, false, st);
         if (r != MOE_OK) return r;
     }
@@ -775,6 +784,8 @@ static int launch_attention(const moe_attn_shape_t &s, AttnParams p, char *ws, c
         p.min_rows = kFewRows + 1;
         p.max_rows = 0x7fffffff;
         p.wait_at_end = 1;
+        p.team_log = 0;
+        p.n_teams = s.n_kv_heads;
         if (attn_tc_takes(s)) {
             items_of(attn_tc_rows(s));
             many = AttnParts{p.part, p.desc, sms, p.tile_rows};

@@ -12,6 +12,8 @@
 //   - its load side runs kSlots - 1 blocks ahead, over the borders of items; a lane
 //     looks up a row's page one block before the row is copied.  Any page size; keys
 //     behind the last one, or on a page outside the cache, become zeros.
+//   - heads with short rows are read side by side: two or four warps take the same
+//     keys of heads next to one another, so that lines and DRAM pages are used whole.
 // Forms that were slower: the block's keys split among four warps with a block
 // barrier per block (4.1 TB/s on the case above), TMA boxes of a page each (4.0 TB/s
 // with 16-token pages, 5.7 with 128-token pages), and load warps filling one ring
@@ -43,9 +45,11 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t ring = smem_u32(smem) + warp * (kSlots * C::kStage);
-    const int unit = warp * gridDim.x + blockIdx.x;
 
     Split<C::kThreads, kRows, kBlk, C::kWarps> split;
+    // the warp's range, its head of a team's, and its place among the partial results:
+    // one head's ranges lie side by side
+    const int range = split.range(p, warp), in_team = warp & ((1 << p.team_log) - 1), unit = in_team * split.ranges(p) + range;
     Cursor<kRows, kBlk> cur;
     const long long n_blocks = split.init(p, cur, reinterpret_cast<long long *>(smem));
     grid_dep_launch();
@@ -53,6 +57,8 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
         if (lane == 0) p.desc[unit].parts = 0;
         return;
     }
+
+    auto head_of = [&](const Cursor<kRows, kBlk> &at) { return (at.kvh << p.team_log) + in_team; };
 
     // ------------------------------------------------------------------ loads
     // Lane r has row r of a block (and row r + 32); a copy takes 32 / kChunks rows.
@@ -73,7 +79,7 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
             const int col = p.by_page.div(key);
             const int id = __ldg(p.table + static_cast<long long>(ld.b) * p.max_pages + col);
             if (id < 0 || id >= p.num_pages) bad = true;
-            else off[j] = (id * p.page_stride + (static_cast<long long>(key - col * p.page_size) * p.n_kv + ld.kvh) * kD) * esz;
+            else off[j] = (id * p.page_stride + (static_cast<long long>(key - col * p.page_size) * p.n_kv + head_of(ld)) * kD) * esz;
         }
         if (--ld_left > 0 && ++ld.blk == ld.nblk) ld.next_item(p);
     };
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
     auto col = [&](int i, int e) { return kE4m3 ? 16 * (i >> 1) + 4 * cq + 2 * e + (i & 1) : 8 * i + 2 * cq + e; };
     auto out_row = [&](int grow) {
         return static_cast<__nv_bfloat16 *>(p.out) + (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
-                                                      cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
+                                                      head_of(cur) * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
     };
     for (;;) {
         const int n = static_cast<int>(min(n_blocks - begin, static_cast<long long>(cur.nblk - cur.blk)));
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
                 const bool real = r < rows;
                 const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
                                            static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.q_stride +
-                                           static_cast<long long>(cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
+                                           static_cast<long long>(head_of(cur) * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
                 lim[h] = real ? row_limit(p, cur.r, grow) : 0;
                 mult[h] = p.scale_log2;
 #pragma unroll
@@ -339,10 +345,10 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
                 AttnDesc d;
                 d.parts = 0;
                 d.qs = cur.r.qs;
-                d.kvh = cur.kvh;
+                d.kvh = head_of(cur);
                 d.row0 = row0;
                 d.rows = rows;
-                if (!last && !continued) d.parts = split.parts(unit, begin - n, cur.nblk);
+                if (!last && !continued) d.parts = split.parts(range, begin - n, cur.nblk);
                 p.desc[unit] = d;
             }
             break;

@@ -84,6 +84,7 @@ struct AttnParams {
     int min_rows, max_rows;   // this kernel's requests: rows in [min_rows, max_rows]
     int tile_rows;            // query rows of an item
     int tile_tokens;          // whole tokens of an item, 0 where tokens are cut
+    int team_log, n_teams;    // 2^team_log heads side by side, n_kv / 2^team_log times
     FastDiv by_group, by_page, by_tile;
     int wait_at_end;          // launched while the kernel before it runs
     float scale_log2, v_scale;
@@ -192,7 +193,8 @@ __device__ __forceinline__ long long request_blocks(const AttnParams &p, const R
     return s;
 }
 
-// A position in the numbering, held by every lane of a warp.
+// A position in the numbering, held by every lane of a warp.  kvh counts teams of
+// heads (see Split).
 template <int kRows, int kBlk>
 struct Cursor {
     Req r;
@@ -214,7 +216,7 @@ struct Cursor {
         blk = 0;
         if (++tile == tiles) {
             tile = 0;
-            if (++kvh == p.n_kv) {
+            if (++kvh == p.n_teams) {
                 kvh = 0;
                 bool bad = false;
                 const int lane = threadIdx.x & 31;
@@ -235,9 +237,10 @@ struct Cursor {
     }
 };
 
-// The division itself.  A CTA has kUnits ranges, one for each of its first kUnits
-// warps (range warp * gridDim.x + blockIdx.x, so that few ranges spread over all
-// SMs), or one for all.  init() finds where the calling thread's range starts (cur)
+// The division itself.  A CTA has one range for all, or its first kUnits warps have
+// ranges of their own.  Then 2^team_log warps side by side are a team with one range,
+// in which each takes another head of the same keys, and teams are what is numbered
+// where it says head (few ranges spread over all SMs).  init() finds where the calling thread's range starts (cur)
 // and returns how many blocks it has; block-collective over kThreads threads, with
 // kThreads words of shared memory to itself meanwhile.
 template <int kThreads, int kRows, int kBlk, int kUnits = 1>
@@ -246,7 +249,15 @@ struct Split {
     int G;                // ranges that share them
 
     __device__ __forceinline__ long long start(int c) const { return div_ll(W * c, G); }
-    static __device__ __forceinline__ int unit(int k) { return k * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); }
+    // the range of warp k
+    static __device__ __forceinline__ int range(const AttnParams &p, int k)
+    {
+        return (kUnits > 1 ? k >> p.team_log : k) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    }
+    static __device__ __forceinline__ int ranges(const AttnParams &p)
+    {
+        return (kUnits > 1 ? kUnits >> p.team_log : 1) * static_cast<int>(gridDim.x);
+    }
 
     __device__ __forceinline__ long long init(const AttnParams &p, Cursor<kRows, kBlk> &cur, long long *s_before)
     {
@@ -257,7 +268,7 @@ struct Split {
         const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
         bool bad = false;
         long long sum = 0;
-        for (int b = b0; b < b1; ++b) sum += p.n_kv * request_blocks<kRows, kBlk>(p, attn_request(p, b, bad));
+        for (int b = b0; b < b1; ++b) sum += p.n_teams * request_blocks<kRows, kBlk>(p, attn_request(p, b, bad));
         if (bad && p.status && blockIdx.x == 0) set_status(p.status, MOE_ERR_DEVICE_CHECK);
         long long inc = sum;
 #pragma unroll
@@ -275,12 +286,12 @@ struct Split {
             W += s_warp[w];
         }
         s_before[tid] = before;
-        const int units = static_cast<int>(gridDim.x) * kUnits;
-        G = W < units ? static_cast<int>(W) : units;
-        if (unit(0) >= G) return 0;                          // none of the CTA's ranges
+        const int most = ranges(p);
+        G = W < most ? static_cast<int>(W) : most;
+        if (range(p, 0) >= G) return 0;                          // none of the CTA's ranges
         __syncthreads();
-        if (warp < kUnits && unit(warp) < G) {
-            long long at = start(unit(warp));
+        if (warp < kUnits && range(p, warp) < G) {
+            long long at = start(range(p, warp));
             // the thread in whose requests it lies: the last one with before <= at
             int lo = 0, hi = kThreads;
             while (hi - lo > 1) {
@@ -295,8 +306,8 @@ struct Split {
             for (;; ++b) {
                 r = attn_request(p, b, bad);
                 per_head = request_blocks<kRows, kBlk>(p, r);
-                if (at < per_head * p.n_kv) break;
-                at -= per_head * p.n_kv;
+                if (at < per_head * p.n_teams) break;
+                at -= per_head * p.n_teams;
             }
             const int kvh = static_cast<int>(div_ll(at, per_head));
             at -= per_head * kvh;
@@ -334,7 +345,7 @@ struct Split {
         }
         __syncthreads();
         const int k = kUnits > 1 ? warp : 0;
-        if (k >= kUnits || unit(k) >= G) return 0;
+        if (k >= kUnits || range(p, k) >= G) return 0;
         cur.b = s_at[k][0];
         cur.kvh = s_at[k][1];
         cur.tile = s_at[k][2];
@@ -342,7 +353,7 @@ struct Split {
         cur.r = attn_request(p, cur.b, bad);
         cur.enter_request(p);
         cur.enter(p);
-        return start(unit(k) + 1) - start(unit(k));
+        return start(range(p, k) + 1) - start(range(p, k));
     }
 
     // Ranges over which the item extends that range c starts at `from_start`

@@ -313,6 +313,13 @@ def test_attention_head_layouts(heads, kv_heads, q, kv):
     _check_attn(ref.Batch(q, kv, heads=heads, kv_heads=kv_heads, dim=128, e4m3=True, seed=2))
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(3, 3), (8, 4), (12, 6), (8, 8), (14, 7), (24, 12), (16, 16), (32, 2)])
+@pytest.mark.parametrize("dim,e4m3", [(64, True), (64, False), (128, True)])
+def test_attention_heads_side_by_side(heads, kv_heads, dim, e4m3):
+    """Numbers of key/value heads that two or four warps share, or cannot."""
+    _check_attn(ref.Batch([1, 1, 2, 0, 1], [200, 1, 1100, 5, 65], heads=heads, kv_heads=kv_heads, dim=dim, e4m3=e4m3, seed=12))
+
+
 @pytest.mark.parametrize("ps", [1, 3, 8, 16, 24, 32, 64, 100, 128, 256, 512])
 def test_attention_page_sizes(ps):
     _check_attn(ref.Batch([1, 60, 1], [130, 300, 600], heads=4, kv_heads=2, dim=128, ps=ps, seed=3))
