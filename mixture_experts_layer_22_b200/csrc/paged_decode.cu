@@ -32,8 +32,10 @@ template <int kD, bool kE4m3>
 struct DecCfg {
     static constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps;
     static constexpr int kRowBytes = kD * (kE4m3 ? 1 : 2), kChunks = kRowBytes / 16;
-    static constexpr int kRows = 16, kBlk = 4096 / kRowBytes;            // 16 to 64 keys: 4 KB of K, 4 KB of V
-    static constexpr int kMat = kBlk * kRowBytes, kStage = 2 * kMat, kSlots = 3;
+    // 4 or 6 KB of K and as many of V: 16, 48 or 96 keys.  Against blocks of 32 and 64
+    // in three slots, those of shorter rows gain 1 to 3% (128 requests, E4M3: 183 to 178 us).
+    static constexpr int kRows = 16, kBlk = kRowBytes == 256 ? 16 : 6144 / kRowBytes, kSlots = kRowBytes == 256 ? 3 : 2;
+    static constexpr int kMat = kBlk * kRowBytes, kStage = 2 * kMat;
     static constexpr int kSmem = kWarps * kSlots * kStage;
 };
 
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
     auto head_of = [&](const Cursor<kRows, kBlk> &at) { return (at.kvh << p.team_log) + in_team; };
 
     // ------------------------------------------------------------------ loads
-    // Lane r has row r of a block (and row r + 32); a copy takes 32 / kChunks rows.
+    // Lane r has row r of a block (and rows r + 32, r + 64); a copy takes 32 / kChunks rows.
     constexpr int kLook = (kBlk + 31) / 32, kAtOnce = 32 / kChunks;
     constexpr int esz = kE4m3 ? 1 : 2;
     Cursor<kRows, kBlk> ld = cur;
