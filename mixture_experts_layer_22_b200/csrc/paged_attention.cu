@@ -371,17 +371,17 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                     if (r < rows) {
                         const int grow = cur.row0(p) + r;
                         if (whole) {
-                            const float inv = l[h] > 0.0f ? p.v_scale / l[h] : l[h] == 0.0f ? 0.0f : l[h];
+                            const float inv = row_inverse(l[h]), vs = p.v_scale;
                             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                                  (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
                                                   cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD;
 #pragma unroll
                             for (int i = 0; i < kD / 8; ++i) {
                                 if constexpr (kE4m3) {
-                                    dst[col(i, 0)] = __float2bfloat16_rn(o[i][2 * h] * inv);
-                                    dst[col(i, 1)] = __float2bfloat16_rn(o[i][2 * h + 1] * inv);
+                                    dst[col(i, 0)] = __float2bfloat16_rn(o[i][2 * h] * inv * vs);
+                                    dst[col(i, 1)] = __float2bfloat16_rn(o[i][2 * h + 1] * inv * vs);
                                 } else {
-                                    *reinterpret_cast<uint32_t *>(dst + col(i, 0)) = bf16x2_of(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+                                    *reinterpret_cast<uint32_t *>(dst + col(i, 0)) = bf16x2_of(o[i][2 * h] * inv * vs, o[i][2 * h + 1] * inv * vs);
                                 }
                             }
                         } else {
@@ -438,14 +438,14 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
                     for (int w = 0; w < kWN; ++w) lt += s_l[w][r] * exp2_fast(s_m[w][r] - base);
                     const float *v = s_merge + r * kD + c;
                     if (whole) {
-                        const float inv = lt > 0.0f ? p.v_scale / lt : lt == 0.0f ? 0.0f : lt;
+                        const float inv = row_inverse(lt), vs = p.v_scale;
                         const int grow = cur.row0(p) + r;
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                              (static_cast<long long>(cur.r.qs + p.by_group.div(grow)) * p.n_heads +
                                               cur.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD + c;
                         *reinterpret_cast<uint4 *>(dst) =
-                            make_uint4(bf16x2_of(v[0] * inv, v[1] * inv), bf16x2_of(v[2] * inv, v[3] * inv),
-                                       bf16x2_of(v[4] * inv, v[5] * inv), bf16x2_of(v[6] * inv, v[7] * inv));
+                            make_uint4(bf16x2_of(v[0] * inv * vs, v[1] * inv * vs), bf16x2_of(v[2] * inv * vs, v[3] * inv * vs),
+                                       bf16x2_of(v[4] * inv * vs, v[5] * inv * vs), bf16x2_of(v[6] * inv * vs, v[7] * inv * vs));
                     } else {
                         float4 *d = reinterpret_cast<float4 *>(part + r * kD + c);
                         d[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -542,13 +542,13 @@ template <int kD>
 __device__ __forceinline__ void put_row(const AttnParams &p, const AttnDesc &d, int r, const float (&acc)[kD / 32], float l)
 {
     constexpr int kE = kD / 32;
-    const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
+    const float inv = row_inverse(l), vs = p.v_scale;
     const int grow = d.row0 + r;
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                          (static_cast<long long>(d.qs + p.by_group.div(grow)) * p.n_heads + d.kvh * p.group + (grow - p.by_group.div(grow) * p.group)) * kD +
                          (threadIdx.x & 31) * kE;
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2_of(acc[e] * inv * vs, acc[e + 1] * inv * vs);
 }
 
 // The same for items of many rows (see many_at): two adjacent rows a lane, kD / 4
@@ -596,14 +596,14 @@ __device__ __forceinline__ void join_rows(const AttnParams &p, const AttnParts &
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (r + j >= d.rows) continue;
-            const float inv = l[j] > 0.0f ? p.v_scale / l[j] : l[j] == 0.0f ? 0.0f : l[j];
+            const float inv = row_inverse(l[j]), vs = p.v_scale;
             const int grow = d.row0 + r + j, tok = p.by_group.div(grow);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                  (static_cast<long long>(d.qs + tok) * p.n_heads + d.kvh * p.group + (grow - tok * p.group)) * kD;
 #pragma unroll
             for (int i = 0; i < kC; ++i)
                 *reinterpret_cast<uint2 *>(dst + 4 * (x + i * kAcross)) =
-                    make_uint2(bf16x2_of(acc[j][i].x * inv, acc[j][i].y * inv), bf16x2_of(acc[j][i].z * inv, acc[j][i].w * inv));
+                    make_uint2(bf16x2_of(acc[j][i].x * inv * vs, acc[j][i].y * inv * vs), bf16x2_of(acc[j][i].z * inv * vs, acc[j][i].w * inv * vs));
         }
     }
 }

@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (last && !continued) {
-                    const float inv = l > 0.0f ? p.v_scale / l : l == 0.0f ? 0.0f : l;
+                    const float inv = row_inverse(l), vs = kLoad == kLoadCodes ? p.v_scale : 1.0f;
                     const int grow = cur.row0(p) + row, tok = p.by_group.div(grow);
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                          (static_cast<long long>(cur.r.qs + tok) * p.n_heads + cur.kvh * p.group + (grow - tok * p.group)) * kD;
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(TcCfg<kD, kLoad>::kThreads, 1)
                             for (int i = 0; i < 32; i += 16) {
                                 uint32_t y[8];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] = bf16x2_of(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
+                                for (int e = 0; e < 8; ++e) y[e] = bf16x2_of(o[i + 2 * e] * inv * vs, o[i + 2 * e + 1] * inv * vs);
                                 put_32b(dst + c + i, y, wide);
                             }
                         }

@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(DecCfg<kD, kE4m3>::kThreads, 1) paged_decode_k
             const int r = r_lo + 8 * h;
             if (r >= rows) continue;
             if (whole) {
-                const float inv = l[h] > 0.0f ? p.v_scale / l[h] : l[h] == 0.0f ? 0.0f : l[h];
+                const float inv = row_inverse(l[h]), vs = kE4m3 ? p.v_scale : 1.0f;
                 __nv_bfloat16 *dst = out_row(row0 + r);
 #pragma unroll
                 for (int i = 0; i < kD / 8; i += 2) {
-                    const float a = o[i][2 * h] * inv, b = o[i][2 * h + 1] * inv, c = o[i + 1][2 * h] * inv, d = o[i + 1][2 * h + 1] * inv;
+                    const float a = o[i][2 * h] * inv * vs, b = o[i][2 * h + 1] * inv * vs, c = o[i + 1][2 * h] * inv * vs,
+                                d = o[i + 1][2 * h + 1] * inv * vs;
                     if constexpr (kE4m3) {
                         *reinterpret_cast<uint2 *>(dst + col(i, 0)) = make_uint2(bf16x2_of(a, c), bf16x2_of(b, d));
                     } else {

@@ -63,6 +63,11 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b)
 // quarter of a million keys of 2^-26 each, 2^-8 together, were.
 constexpr float kF16Up = 15.0f, kF16UpLag = 7.0f;
 
+// What a row's sums are divided by: 0 for a row that sees nothing.  A cache's scale is
+// a factor of its own behind it, since their quotient may be too small for fp32 where
+// neither the sum nor the result is.
+__device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l; }
+
 __device__ __forceinline__ uint32_t f16x2_of(float a, float b)
 {
     const __half2 r = __floats2half2_rn(a, b);

@@ -534,6 +534,23 @@ def test_attention_many_small_weights_beside_a_large_one(e4m3, dim, n, heads, at
     assert ((out.cpu().double().reshape(B, n, heads, dim) - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("v_scale", [1e-37, 1e35])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("requests", [1, 300])
+def test_attention_extreme_value_scales(dim, v_scale, requests):
+    """Scales at which a scale over a row's sum is below fp32's normal numbers, and the
+    outputs are not; items cut among many ranges, and whole ones."""
+    b = ref.Batch([1, 40] * requests, [4000 if requests == 1 else 70, 300 if requests == 1 else 60] * requests, heads=2, kv_heads=1,
+                  dim=dim, e4m3=True, seed=13)
+    d = Dev(b)
+    d.shape.v_scale = v_scale
+    out = d.run().cpu().double()
+    want, tol = b.reference()
+    by = d.shape.v_scale / b.kv_scale
+    # the values' bound, times the scale, and a rounding more
+    assert ((out - want * by).abs() <= (tol + 2 * ref.U_F32 * want.abs()) * by).all()
+
+
 def test_binding_refuses_wrong_tensors():
     d = Dev(ref.Batch([1], [20], heads=4, kv_heads=2, dim=64))
     args = dict(q=d.q, k_cache=d.k_cache, v_cache=d.v_cache, block_table=d.table, q_start=d.q_start, kv_len=d.kv_len, out=d.out,
