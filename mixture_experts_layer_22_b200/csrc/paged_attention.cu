@@ -564,13 +564,15 @@ __device__ __forceinline__ void join_rows(const AttnParams &p, const AttnParts &
     auto part = [&](int k) { return from.part + (k == 0 ? 2LL * c + 1 : 2LL * (c + k)) * stride; };
     for (int r0 = row0 + (threadIdx.x >> 5) * kStep; r0 < min(d.rows, behind); r0 += 8 * kStep) {
         const int r = r0 + 2 * (lane / kAcross), at_m = from.rows * kD + r, at_l = at_m + from.rows;
+        if (r >= d.rows) continue;               // no lane waits for another here
         float base[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         float4 acc[2][kC];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < kC; ++i) acc[j][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        // the rows are even, so that both have a place even where the second is none of the item's
+        // from.rows and r are even and r is a row of the item's: the second has a place in
+        // the part even where it is none of the item's
 #pragma unroll 4
         for (int k = 0; k < d.parts; ++k) {
             base[0] = fmaxf(base[0], part(k)[at_m]);
