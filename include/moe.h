@@ -478,7 +478,8 @@ int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes);
  *   or not ascending is skipped.
  * The result of a call does not depend on what else runs or ran (the work split
  * depends on the batch's lengths and the device alone; no atomics).
- * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (other head_dim),
+ * Errors: MOE_ERR_INVALID_ARG (out, the workspace or the status over another
+ * buffer of the call included), MOE_ERR_UNSUPPORTED (other head_dim),
  * MOE_ERR_WORKSPACE_TOO_SMALL.  A pipeline wait that runs out sets the status
  * to MOE_ERR_TIMEOUT.  Asynchronous on `stream`.
  */

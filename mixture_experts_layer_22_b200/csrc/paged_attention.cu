@@ -17,6 +17,7 @@
 // 130 to 160 TFLOP/s on prompts at head_dim 128.
 #include <atomic>
 
+#include "overlap.cuh"
 #include "paged_mma.cuh"
 #include "paged_work.cuh"
 
@@ -860,7 +861,27 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
         (reinterpret_cast<uintptr_t>(ws) & 255))
         return MOE_ERR_INVALID_ARG;
     if (ws_bytes < attn_ws(s).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-    if (out == q) return MOE_ERR_INVALID_ARG;
+    const int64_t q_row = static_cast<int64_t>(s.n_heads) * s.head_dim, page_row = static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim;
+    const int64_t q_stride = s.q_stride ? s.q_stride : q_row, page_stride = s.page_stride ? s.page_stride : page_row;
+    {
+        // What the kernels write lies over nothing that they read, and over nothing else
+        // that they write: other CTAs still read a request's queries when its first rows
+        // are stored.
+        const int64_t esz = s.cache_dtype == MOE_E4M3 ? 1 : 2;
+        const Extent read[] = {{q, q_row * 2, q_stride * 2, s.num_tokens},
+                               {k_cache, page_row * esz, page_stride * esz, s.num_pages},
+                               {v_cache, page_row * esz, page_stride * esz, s.num_pages},
+                               {block_table, static_cast<int64_t>(s.B) * s.max_pages * 4},
+                               {q_start, (s.B + 1) * 4ll},
+                               {kv_len, s.B * 4ll}};
+        const Extent written[] = {{out, q_row * 2 * s.num_tokens}, {ws, static_cast<int64_t>(attn_ws(s).total)}, {status, 4}};
+        for (int i = 0; i < 3; ++i) {
+            for (const Extent &r : read)
+                if (overlap(written[i], r)) return MOE_ERR_INVALID_ARG;
+            for (int j = 0; j < i; ++j)
+                if (overlap(written[i], written[j])) return MOE_ERR_INVALID_ARG;
+        }
+    }
     AttnParams p;
     p.q = q;
     p.k_cache = k_cache;
@@ -870,8 +891,8 @@ extern "C" int moe_paged_attention(const moe_attn_shape_t *shape, const void *q,
     p.kv_len = kv_len;
     p.out = out;
     p.status = status;
-    p.q_stride = s.q_stride ? s.q_stride : static_cast<int64_t>(s.n_heads) * s.head_dim;
-    p.page_stride = s.page_stride ? s.page_stride : static_cast<int64_t>(s.page_size) * s.n_kv_heads * s.head_dim;
+    p.q_stride = q_stride;
+    p.page_stride = page_stride;
     p.B = s.B;
     p.T = s.num_tokens;
     p.n_heads = s.n_heads;
