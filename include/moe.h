@@ -416,8 +416,10 @@ typedef struct {
  *   A slot below -1 or at or above num_pages * page_size, or a position outside
  *   [0, max_pos) with rot_dim > 0, sets the status and the token is skipped in
  *   the same way.  Slots of one call must differ: of two tokens with the same
- *   slot either may be found there, in parts.
- * Errors: MOE_ERR_INVALID_ARG (bad sizes, NULL or misaligned pointers),
+ *   slot either may be found there, in parts.  k_cache and v_cache may be one
+ *   buffer where every token's rotated k and its v are the same.
+ * Errors: MOE_ERR_INVALID_ARG (bad sizes, NULL or misaligned pointers, q_out, a
+ * cache or the status over another buffer of the call but as said here),
  * MOE_ERR_UNSUPPORTED (other head_dim or rot_dim).  Asynchronous on `stream`.
  */
 int moe_rope_append(const moe_append_shape_t *shape, const void *q, const void *k, const void *v,

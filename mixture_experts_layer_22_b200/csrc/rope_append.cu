@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 
@@ -233,6 +234,28 @@ extern "C" int moe_rope_append(const moe_append_shape_t *shape, const void *q, c
         misaligned(v_cache, 16) || misaligned(cos_sin, 4))
         return MOE_ERR_INVALID_ARG;
     if (q == q_out && p.qs != q_row) return MOE_ERR_INVALID_ARG;
+    {
+        // What the kernel writes lies over nothing else: the warps read and write tokens
+        // and heads in any order.  In place, a lane writes only what it has read itself;
+        // one cache for both is the caller's statement that k and v are the same.
+        const int64_t esz = s.cache_dtype == MOE_E4M3 ? 1 : 2, n = s.num_tokens, rot = s.rot_dim > 0;
+        const Extent written[] = {{q_out, q_row * 2 * n},
+                                  {k_cache, kv_row * s.page_size * esz, p.page_stride * esz, s.num_pages},
+                                  {v_cache, kv_row * s.page_size * esz, p.page_stride * esz, s.num_pages},
+                                  {status, 4}};
+        const Extent read[] = {{q, q_row * 2, p.qs * 2, n},
+                               {k, kv_row * 2, p.ks * 2, n},
+                               {v, kv_row * 2, p.vs * 2, n},
+                               {slots, 4 * n},
+                               {positions, 4 * n * rot},
+                               {cos_sin, 4ll * s.max_pos * s.rot_dim * rot}};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 6; ++j)
+                if (overlap(written[i], read[j]) && !(i == 0 && j == 0 && q_out == q)) return MOE_ERR_INVALID_ARG;
+            for (int j = 0; j < i; ++j)
+                if (overlap(written[i], written[j]) && !(i == 2 && j == 1 && v_cache == k_cache)) return MOE_ERR_INVALID_ARG;
+        }
+    }
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.v = static_cast<const __nv_bfloat16 *>(v);

@@ -94,3 +94,72 @@ def test_attention_takes_buffers_between_the_rows_of_others(lib):
     assert _attention(lib, gaps, v_cache=k + 2 * page, out=k + 2 * 2 * page - 16) == INVALID
     assert _attention(lib, gaps, v_cache=k + 2 * page, out=k + 2 * 9 * 4 * page + 16) == INVALID
     assert _attention(lib, v_cache=k) == NO_GPU
+
+
+# ---------------------------------------------------------------- the append
+APPEND = dict(num_tokens=8, n_heads=8, n_kv_heads=2, head_dim=128, rot_dim=128, max_pos=64, interleaved=0, page_size=16,
+              num_pages=64, cache_dtype=0, k_scale=1.0, v_scale=1.0)
+APPEND_AT = _apart(["q", "k", "v", "positions", "slots", "cos_sin", "q_out", "k_cache", "v_cache", "status"])
+
+
+def _append(lib, shape=None, **at):
+    s = moe.AppendShape(**{**APPEND, **(shape or {})})
+    p = {**APPEND_AT, **at}
+    return lib.moe_rope_append(C.byref(s), *(p[n] for n in APPEND_AT), None)
+
+
+def _append_bytes(shape=None):
+    a = {**APPEND, **(shape or {})}
+    esz, n = 1 if a["cache_dtype"] else 2, a["num_tokens"]
+    q, kv = a["n_heads"] * a["head_dim"], a["n_kv_heads"] * a["head_dim"]
+    page = a["page_size"] * kv
+    cache = esz * ((a["num_pages"] - 1) * (a.get("page_stride") or page) + page)
+    rows = {x: 2 * ((n - 1) * (a.get(x + "_stride") or w) + w) for x, w in (("q", q), ("k", kv), ("v", kv))}
+    return dict(**rows, positions=4 * n, slots=4 * n, cos_sin=4 * a["max_pos"] * a["rot_dim"], q_out=2 * n * q, k_cache=cache,
+                v_cache=cache, status=4)
+
+
+@pytest.mark.parametrize("shape", [{}, dict(cache_dtype=1), dict(q_stride=12 * 128, k_stride=12 * 128, v_stride=12 * 128),
+                                   dict(page_stride=2 * 16 * 2 * 128)], ids=str)
+@pytest.mark.parametrize("written,align", [("q_out", 16), ("k_cache", 16), ("v_cache", 16), ("status", 4)])
+@pytest.mark.parametrize("over", list(APPEND_AT))
+def test_append_writes_over_nothing_else(lib, shape, written, align, over):
+    if written == over:
+        return
+    n = _append_bytes(shape)
+    assert _append(lib, shape) == NO_GPU
+    at = APPEND_AT[over]
+    step = align if over != "q" or written != "q_out" else 2 * align
+    for x in (at, (at + n[over] - 1) // align * align, _up(at - n[written] + 1, align), at + step):
+        if x >= at + n[over] or (x == at and {written, over} in ({"q_out", "q"}, {"k_cache", "v_cache"})):
+            continue                                     # behind it, or one of the two forms that are allowed
+        assert _append(lib, shape, **{written: x}) == INVALID
+    for x in (_up(at + n[over], align), (at - n[written]) // align * align):
+        assert _append(lib, shape, **{written: x}) == NO_GPU
+
+
+def test_append_in_place_and_one_cache(lib):
+    """q_out on q where q's rows are adjacent, one cache for both; neither shifted."""
+    row, page = 8 * 128 * 2, 16 * 2 * 128 * 2
+    assert _append(lib, q_out=APPEND_AT["q"]) == NO_GPU
+    assert _append(lib, dict(q_stride=12 * 128), q_out=APPEND_AT["q"]) == INVALID
+    for shift in (-row, -256, 256, row):
+        assert _append(lib, q_out=APPEND_AT["q"] + shift) == INVALID
+    assert _append(lib, v_cache=APPEND_AT["k_cache"]) == NO_GPU
+    for shift in (-page, -256, 256, page):
+        assert _append(lib, v_cache=APPEND_AT["k_cache"] + shift) == INVALID
+
+
+def test_append_takes_alternating_pages_and_unread_tables(lib):
+    page = 16 * 2 * 128
+    k = APPEND_AT["k_cache"]
+    assert _append(lib, dict(page_stride=2 * page), v_cache=k + 2 * page) == NO_GPU
+    assert _append(lib, dict(page_stride=2 * page), v_cache=k + 2 * page - 16) == INVALID
+    assert _append(lib, dict(page_stride=2 * page, cache_dtype=1), v_cache=k + page) == NO_GPU
+    # without a rotation the positions and the table are not read
+    assert _append(lib, dict(rot_dim=0), positions=APPEND_AT["q_out"], cos_sin=APPEND_AT["k_cache"]) == NO_GPU
+    # a fused projection's rows, one buffer for q, k and v
+    st = dict(q_stride=12 * 128, k_stride=12 * 128, v_stride=12 * 128)
+    q = APPEND_AT["q"]
+    assert _append(lib, st, k=q + 8 * 256, v=q + 10 * 256) == NO_GPU
+    assert _append(lib, {**st, "num_tokens": 1}, k=q + 8 * 256, v=q + 10 * 256, q_out=q + 12 * 256) == NO_GPU
