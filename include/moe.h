@@ -364,7 +364,8 @@ typedef struct {
  *     slots     [max_tokens]  that position's cache slot
  *     free_next [1]           *free_pos + pages taken
  *   Padding rows get position 0 and slot -1.  free_next may be NULL.  An output
- *   that overlaps an input (kv_len on cached, free_next on free_pos) is refused.
+ *   or status over an input (kv_len on cached, free_next on free_pos) or over
+ *   another output is refused.
  *   Bad data sets the status, and: a request with a negative length or with
  *   cached + fresh > max_pages * page_size counts as cached = fresh = 0; a page
  *   that cannot be had (the free list has run out, or its id is outside

@@ -13,6 +13,7 @@
 // token's slot comes from the free list where its page is new and from the
 // table where its page was held before, so no block reads what another writes.
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace moe {
 
@@ -192,19 +193,17 @@ extern "C" int moe_page_plan(const moe_page_shape_t *shape, const int32_t *cache
     if (!cached || !fresh || !block_table || !q_start || !kv_len) return MOE_ERR_INVALID_ARG;
     if (s.max_tokens > 0 && (!positions || !slots)) return MOE_ERR_INVALID_ARG;
     if (s.n_free > 0 && !free_pages) return MOE_ERR_INVALID_ARG;
-    // Blocks read the inputs while others write: no output may lie over an input.
-    struct Words {
-        const int32_t *at;
-        int64_t n;
-    };
-    const Words in[] = {{cached, s.B}, {fresh, s.B}, {free_pages, s.n_free}, {free_pos, 1}};
-    const Words out[] = {{block_table, static_cast<int64_t>(s.B) * s.max_pages}, {q_start, s.B + 1}, {kv_len, s.B},
-                         {positions, s.max_tokens}, {slots, s.max_tokens}, {free_next, 1}};
-    for (const Words &i : in)
-        for (const Words &o : out)
-            if (i.at && o.at && reinterpret_cast<uintptr_t>(i.at) < reinterpret_cast<uintptr_t>(o.at + o.n) &&
-                reinterpret_cast<uintptr_t>(o.at) < reinterpret_cast<uintptr_t>(i.at + i.n))
-                return MOE_ERR_INVALID_ARG;
+    // Blocks read the inputs while others write: no output may lie over an input, nor over
+    // another output.
+    const Extent in[] = {{cached, s.B * 4ll}, {fresh, s.B * 4ll}, {free_pages, s.n_free * 4ll}, {free_pos, 4}};
+    const Extent out[] = {{block_table, static_cast<int64_t>(s.B) * s.max_pages * 4}, {q_start, (s.B + 1) * 4ll}, {kv_len, s.B * 4ll},
+                          {positions, s.max_tokens * 4ll}, {slots, s.max_tokens * 4ll}, {free_next, 4}, {status, 4}};
+    for (int i = 0; i < 7; ++i) {
+        for (const Extent &e : in)
+            if (overlap(out[i], e)) return MOE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return MOE_ERR_INVALID_ARG;
+    }
     // One row per thread up to a block per SM.  New pages are at most a page
     // per token plus the rows that max_tokens cuts off; the loops stride.
     const int want = (s.max_tokens + kPlanThreads - 1) / kPlanThreads;

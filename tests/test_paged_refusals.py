@@ -163,3 +163,29 @@ def test_append_takes_alternating_pages_and_unread_tables(lib):
     q = APPEND_AT["q"]
     assert _append(lib, st, k=q + 8 * 256, v=q + 10 * 256) == NO_GPU
     assert _append(lib, {**st, "num_tokens": 1}, k=q + 8 * 256, v=q + 10 * 256, q_out=q + 12 * 256) == NO_GPU
+
+
+# ------------------------------------------------------------------ the plan
+PLAN = dict(B=4, max_tokens=16, max_pages=8, page_size=16, num_pages=64, n_free=10)
+PLAN_AT = _apart(["cached", "fresh", "free_pages", "free_pos", "block_table", "q_start", "kv_len", "positions", "slots", "free_next",
+                  "status"])
+PLAN_WORDS = dict(cached=4, fresh=4, free_pages=10, free_pos=1, block_table=32, q_start=5, kv_len=4, positions=16, slots=16,
+                  free_next=1, status=1)
+
+
+def _plan(lib, shape=None, **at):
+    p = {**PLAN_AT, **at}
+    return lib.moe_page_plan(C.byref(moe.PageShape(**{**PLAN, **(shape or {})})), *(p[n] for n in PLAN_AT), None)
+
+
+@pytest.mark.parametrize("written", list(PLAN_AT)[4:])
+@pytest.mark.parametrize("over", list(PLAN_AT))
+def test_plan_writes_over_nothing_else(lib, written, over):
+    if written == over:
+        return
+    assert _plan(lib) == NO_GPU
+    at, n, m = PLAN_AT[over], 4 * PLAN_WORDS[over], 4 * PLAN_WORDS[written]
+    for x in (at, at + n - 4, at - m + 4):
+        assert _plan(lib, **{written: x}) == INVALID
+    for x in (at + n, at - m):
+        assert _plan(lib, **{written: x}) == NO_GPU
