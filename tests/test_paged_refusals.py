@@ -2,6 +2,7 @@
 buffer of the unchanged call has addresses of its own, and that call is refused by
 nothing but the missing GPU."""
 import ctypes as C
+import math
 
 import pytest
 import torch
@@ -13,7 +14,7 @@ from mixture_experts_layer_22_b200 import build as mbuild
 # be launched.
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: for hosts without a GPU")
 
-INVALID, NO_GPU = -1, -4          # MOE_ERR_INVALID_ARG, MOE_ERR_CUDA
+INVALID, UNSUPPORTED, TOO_SMALL, NO_GPU = -1, -2, -3, -4          # MOE_ERR_*; the last is what a launch gives here
 
 
 @pytest.fixture(scope="module")
@@ -189,3 +190,90 @@ def test_plan_writes_over_nothing_else(lib, written, over):
         assert _plan(lib, **{written: x}) == INVALID
     for x in (at + n, at - m):
         assert _plan(lib, **{written: x}) == NO_GPU
+
+
+@pytest.mark.parametrize("kw", [dict(B=0), dict(B=-1), dict(B=4097), dict(max_tokens=-1), dict(max_tokens=(1 << 30) + 1), dict(max_pages=0),
+                                dict(page_size=0), dict(num_pages=0), dict(n_free=-1), dict(num_pages=1 << 20, page_size=1 << 11),
+                                dict(max_pages=1 << 20, page_size=1 << 11)], ids=str)
+def test_plan_refuses_each_bad_size(lib, kw):
+    assert _plan(lib) == NO_GPU
+    # far apart: some of these sizes would reach the next buffer
+    far = {n: a << 16 for n, a in PLAN_AT.items()}
+    assert _plan(lib, **far) == NO_GPU and _plan(lib, kw, **far) == INVALID
+
+
+@pytest.mark.parametrize("name", ["cached", "fresh", "free_pages", "block_table", "q_start", "kv_len", "positions", "slots"])
+def test_plan_refuses_each_null(lib, name):
+    assert _plan(lib, **{name: None}) == INVALID
+
+
+def test_plan_takes_what_may_be_missing(lib):
+    for name in ("free_pos", "free_next", "status"):
+        assert _plan(lib, **{name: None}) == NO_GPU
+    assert _plan(lib, dict(n_free=0), free_pages=None) == NO_GPU
+    assert _plan(lib, dict(max_tokens=0), positions=None, slots=None) == NO_GPU
+    # the cursor is not its own successor, and that alone is refused
+    assert _plan(lib, free_next=PLAN_AT["free_pos"]) == INVALID
+    assert lib.moe_page_plan(None, *PLAN_AT.values(), None) == INVALID
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(num_tokens=-1), -1), (dict(n_heads=0), -1), (dict(n_heads=65537), -1), (dict(n_kv_heads=0), -1), (dict(n_kv_heads=65537), -1),
+    (dict(rot_dim=-2), -1), (dict(rot_dim=130), -1), (dict(rot_dim=7), -1), (dict(rot_dim=24), -2), (dict(max_pos=0), -1),
+    (dict(interleaved=2), -1), (dict(page_size=0), -1), (dict(num_pages=0), -1), (dict(cache_dtype=2), -1),
+    (dict(head_dim=96, rot_dim=96), -2), (dict(q_stride=1016), -1), (dict(q_stride=1028), -1), (dict(k_stride=128), -1),
+    (dict(k_stride=260), -1), (dict(v_stride=128), -1), (dict(v_stride=260), -1), (dict(page_stride=4088), -1),
+    (dict(page_stride=4080), -1), (dict(page_stride=4104), -1), (dict(cache_dtype=1, k_scale=0.0), -1),
+    (dict(cache_dtype=1, v_scale=-1.0), -1), (dict(cache_dtype=1, k_scale=math.nan), -1), (dict(cache_dtype=1, v_scale=math.nan), -1),
+    (dict(cache_dtype=1, k_scale=math.inf), -1), (dict(cache_dtype=1, v_scale=math.inf), -1), (dict(num_pages=1 << 27), -1),
+    (dict(q_stride=1 << 62), -1), (dict(k_stride=1 << 62), -1), (dict(v_stride=1 << 62), -1), (dict(page_stride=1 << 62), -1)], ids=str)
+def test_append_refuses_each_bad_size(lib, kw, code):
+    far = {n: a << 16 for n, a in APPEND_AT.items()}
+    assert _append(lib, **far) == NO_GPU and _append(lib, kw, **far) == code
+
+
+def test_append_refuses_each_null_and_misaligned(lib):
+    for name in list(APPEND_AT)[:-1]:
+        assert _append(lib, **{name: None}) == INVALID
+    for name in ("q", "k", "v", "q_out", "k_cache", "v_cache"):
+        assert _append(lib, **{name: APPEND_AT[name] + 8}) == INVALID
+    assert _append(lib, cos_sin=APPEND_AT["cos_sin"] + 2) == INVALID
+    assert lib.moe_rope_append(None, *APPEND_AT.values(), None) == INVALID
+    assert _append(lib, status=None) == NO_GPU
+    assert _append(lib, dict(rot_dim=0), positions=None, cos_sin=None) == NO_GPU
+    assert _append(lib, dict(num_tokens=0), **{n: None for n in APPEND_AT}) == 0
+
+
+BAD_ATTN = [
+    (dict(B=0), -1), (dict(B=4097), -1), (dict(num_tokens=-1), -1), (dict(n_heads=0), -1), (dict(n_heads=9), -1),
+    (dict(n_heads=65538), -1), (dict(n_kv_heads=0), -1), (dict(n_kv_heads=3), -1), (dict(head_dim=96), -2), (dict(page_size=0), -1),
+    (dict(num_pages=0), -1), (dict(max_pages=0), -1), (dict(causal=2), -1), (dict(max_q=-1), -1), (dict(cache_dtype=2), -1),
+    (dict(q_stride=1000), -1), (dict(q_stride=1016), -1), (dict(q_stride=1028), -1), (dict(page_stride=4080), -1),
+    (dict(page_stride=4104), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(scale=-math.inf), -1),
+    (dict(cache_dtype=1, k_scale=0.0), -1), (dict(cache_dtype=1, k_scale=math.inf), -1), (dict(cache_dtype=1, v_scale=math.nan), -1),
+    (dict(cache_dtype=1, v_scale=-1.0), -1), (dict(num_pages=1 << 27), -1), (dict(max_pages=1 << 27), -1), (dict(q_stride=1 << 62), -1),
+    (dict(page_stride=1 << 62), -1), (dict(num_tokens=1 << 29), -1)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_ATTN, ids=str)
+def test_attention_refuses_each_bad_size(lib, kw, code):
+    s = moe.AttnShape(**{**ATTN, **kw})
+    far = {n: a << 16 for n, a in ATTN_AT.items()}
+    assert _attention(lib, ws_bytes=1 << 40, **far) == NO_GPU
+    assert lib.moe_attn_workspace_size(C.byref(s), C.byref(C.c_size_t())) == code
+    assert _attention(lib, kw, ws_bytes=1 << 40, **far) == code
+
+
+def test_attention_refuses_each_null_misaligned_and_small(lib):
+    for name in ("q", "k_cache", "v_cache", "block_table", "q_start", "kv_len", "out", "ws"):
+        assert _attention(lib, **{name: None}) == INVALID
+    for name in ("q", "k_cache", "v_cache", "out"):
+        assert _attention(lib, **{name: ATTN_AT[name] + 8}) == INVALID
+    for off in (8, 16, 128):
+        assert _attention(lib, ws=ATTN_AT["ws"] + off) == INVALID
+    need = moe.attn_workspace_size(moe.AttnShape(**ATTN))
+    assert _attention(lib, ws_bytes=need - 1) == TOO_SMALL and _attention(lib, ws_bytes=need) == NO_GPU
+    assert _attention(lib, status=None) == NO_GPU
+    assert lib.moe_paged_attention(None, *ATTN_AT.values(), need, None) == INVALID
+    assert lib.moe_attn_workspace_size(C.byref(moe.AttnShape(**ATTN)), None) == INVALID
+    assert _attention(lib, dict(num_tokens=0), ws_bytes=0, **{n: None for n in ATTN_AT}) == 0
