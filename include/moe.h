@@ -464,9 +464,10 @@ int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes);
  * already, over the cache: for each new token t of request b and query head h
  *   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
  * over the keys j the token sees.  Scores, the softmax's maximum and sum and
- * the accumulation are fp32; p enters its product with v in 16 bits (bf16, fp16
- *   with an E4M3 cache; as two bf16, a high and a low part, for requests with at
- *   most 16 query rows a key/value head and head_dim up to 128).
+ * the accumulation are fp32; p enters its product with v in 16 bits: fp16 with an
+ * E4M3 cache; with a bf16 cache bf16, and as two bf16, a high and a low part, for
+ * requests with at most 16 query rows a key/value head (for all requests where
+ * max_q says that there are no others).
  *   q [num_tokens, n_heads, head_dim] bf16 (16-byte aligned), k_cache, v_cache
  *   (16-byte aligned), block_table [B, max_pages], q_start [B+1], kv_len [B] in;
  *   out [num_tokens, n_heads, head_dim] bf16 (16-byte aligned) out.

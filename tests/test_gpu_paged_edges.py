@@ -3,6 +3,7 @@ places that a first version got wrong or that its tests could not tell apart."""
 import pytest
 import torch
 
+import paged_cases as cases
 import paged_ref as ref
 from test_gpu_paged import Dev, _check_attn
 
@@ -32,3 +33,34 @@ def test_joining_reads_nothing_of_an_unwritten_neighbour(group):
     out = d.run().cpu().double()
     want, tol = b.reference()
     assert int(d.status[0]) == 0 and ((out - want).abs() <= tol).all()
+
+
+# ------------------------------------------- weights in two parts beside a bf16 cache
+def _check_two_parts(b, max_q=None):
+    d = Dev(b, max_q)
+    out = d.run().cpu().double()
+    n = sum(b.q_lens)
+    want, tol = b.reference(cases.U_TWO_BF16)
+    err = (out[:n] - want).abs()
+    assert int(d.status[0]) == 0 and (err <= tol).all(), f"{float((err / tol).max()):.2f} of the bound"
+
+
+@pytest.mark.parametrize("x", [1 - 2.0 ** -9, 0.7519, 0.3])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 8, 64), (8, 1, 128), (16, 1, 128), (4, 2, 256), (16, 1, 256)])
+def test_few_rows_keep_both_parts_of_a_weight(heads, kv_heads, dim, x):
+    """Up to 16 query rows a key/value head: sums of 2^-8 of their terms."""
+    few = 16 * kv_heads // heads
+    _check_two_parts(cases.cancelling([1, min(few, 3), 1, 1, few], [2, 48, 1001, 130, 300], x, heads=heads, kv_heads=kv_heads, dim=dim,
+                                      seed=22))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_hint_of_few_rows_keeps_both_parts_in_all(dim):
+    _check_two_parts(cases.cancelling([40, 1, 17], [90, 300, 701], 0.7519, heads=4, kv_heads=2, dim=dim, seed=23), max_q=1)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q,kv", [([1], [1]), ([1, 1, 1, 1], [1, 17, 64, 300]), ([1] * 6, [2000, 1, 65, 700, 3, 129]),
+                                  ([6, 3], [4, 3]), ([2, 3, 4, 1], [128, 64, 256, 192])])
+def test_few_rows_of_ordinary_batches_within_the_bound_of_two_parts(q, kv, dim):
+    _check_two_parts(ref.Batch(q, kv, heads=4, kv_heads=2, dim=dim, seed=24))
