@@ -493,12 +493,14 @@ int moe_paged_attention(const moe_attn_shape_t *shape, const void *q, const void
 
 /*
  * Self-test of the failure path (no counterpart on the pages): launches one
- * block whose two bounded pipeline waits run out, because nothing arrives on
- * their barriers.  The first gives up after the library's wait limit (2 s),
- * raises the block's abort flag, and the second then gives up at once.  The
- * block writes MOE_ERR_TIMEOUT to the status word at the start of `ws` and
- * exits, so the CUDA context stays usable.  gave_up (device int32) receives
- * the number of waits that gave up (2).  Asynchronous on `stream`.
+ * block of two warps whose bounded pipeline waits run out, because nothing
+ * arrives on their barriers.  One warp gives up after the library's wait limit
+ * (2 s) and raises the block's abort flag, and the other then gives up at once;
+ * first in the wait of the grouped GEMMs, then in that of the paged attention
+ * (about 4 s in all).  The block writes MOE_ERR_TIMEOUT to the status word at
+ * the start of `ws` and exits, so the CUDA context stays usable.  gave_up
+ * (device int32) receives the number of warps that gave up in both (2).
+ * Asynchronous on `stream`.
  */
 int moe_selftest_wait_timeout(void *ws, int32_t *gave_up, moe_stream_t stream);
 

@@ -356,8 +356,9 @@ def paged_attention(shape, q, k_cache, v_cache, block_table, q_start, kv_len, ou
 
 
 def selftest_wait_timeout(ws, gave_up, stream=None):
-    """Launch the failure-path self-test (about 2 s on the GPU): its bounded
-    waits run out and it reports MOE_ERR_TIMEOUT in ws's status word."""
+    """Launch the failure-path self-test (about 4 s on the GPU): its bounded
+    waits, of the grouped GEMMs and of the paged attention, run out and it
+    reports MOE_ERR_TIMEOUT in ws's status word."""
     _check(lib().moe_selftest_wait_timeout(_ptr(ws), _ptr(gave_up), _stream(stream)), "moe_selftest_wait_timeout")
 
 

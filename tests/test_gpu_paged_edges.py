@@ -1,8 +1,11 @@
 """GPU tests of the paged-attention operators beyond those beside their forms:
 places that a first version got wrong or that its tests could not tell apart."""
+import time
+
 import pytest
 import torch
 
+import mixture_experts_layer_22_b200 as moe
 import paged_cases as cases
 import paged_ref as ref
 from test_gpu_paged import Dev, _check_attn
@@ -64,3 +67,22 @@ def test_a_hint_of_few_rows_keeps_both_parts_in_all(dim):
                                   ([6, 3], [4, 3]), ([2, 3, 4, 1], [128, 64, 256, 192])])
 def test_few_rows_of_ordinary_batches_within_the_bound_of_two_parts(q, kv, dim):
     _check_two_parts(ref.Batch(q, kv, heads=4, kv_heads=2, dim=dim, seed=24))
+
+
+# -------------------------------------------------------------- the failure path
+def test_the_attentions_bounded_wait_runs_out_and_the_context_stays_usable():
+    """Both kinds of wait on barriers that nothing arrives on, one after the other: each
+    lasts its limit of 2 s, either's abort flag ends the other warp's wait, and the
+    status is MOE_ERR_TIMEOUT."""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    gave_up = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    b = ref.Batch([70, 1], [200, 90], heads=4, kv_heads=2, dim=64, seed=25)
+    before = Dev(b).run().clone()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    moe.selftest_wait_timeout(ws, gave_up)
+    torch.cuda.synchronize()
+    dt = time.perf_counter() - t0
+    assert int(gave_up[0]) == 2 and int(ws[:4].view(torch.int32)[0]) == -6
+    assert 3.9 < dt < 30.0                               # two clocks
+    assert torch.equal(Dev(b).run(), before)
