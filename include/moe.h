@@ -310,11 +310,18 @@ int moe_inv_rope_quant_per_head(const moe_rope_shape_t *shape, const void *x, co
 
 /*
  * Attention side: a paged key/value cache, from request lengths to attention
- * output (no counterpart on the pages: the steps between two MoE layers of a
- * served decoder that come before moe_inv_rope_quant_per_head).
+ * output (no counterpart on the pages: steps between two MoE layers of a served
+ * decoder).
  *   moe_page_plan        block tables, positions and cache slots of a batch
  *   moe_rope_append      rotary embedding of q and k, k and v into their slots
  *   moe_paged_attention  attention of the batch's new tokens over the cache
+ * The values that moe_rope_append stores carry no rotation, so the attention's
+ * output carries none either: it goes to the output projection as it is, and
+ * moe_inv_rope_quant_per_head does not belong behind it.  That step belongs where
+ * the rotated keys are the values too (one head that keys and values share): with
+ * k_cache given as both caches to moe_paged_attention, out = sum p_j R(x_j) k_j,
+ * and turning it back by the token's own position x leaves
+ * sum p_j R(x_j - x) k_j, a function of distances alone.
  * Shared by the three:
  *   - A batch is B requests.  Request b has cached[b] tokens in the cache and
  *     brings fresh[b] more (0, 1 or a whole prompt).  The new tokens of all
@@ -402,8 +409,8 @@ typedef struct {
 } moe_append_shape_t;
 
 /*
- * Rotary embedding fused with the cache write, one launch (the rotation that
- * moe_inv_rope_quant_per_head takes back): every pair of a q or k head becomes
+ * Rotary embedding fused with the cache write, one launch (of q and k the rotation
+ * that moe_inv_rope_quant_per_head takes back): every pair of a q or k head becomes
  *   a' = a c - b s,  b' = b c + a s
  * with c, s from row positions[t] of cos_sin (layout as there), fp32
  * arithmetic, elements from rot_dim on unrotated.

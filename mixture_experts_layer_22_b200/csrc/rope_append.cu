@@ -1,6 +1,6 @@
 // rope_append.cu - rotary embedding of q and k fused with the write of k and v
-// into a paged cache (moe_rope_append), the forward counterpart of the inverse
-// rotary step.
+// into a paged cache (moe_rope_append); of q and k the rotation that the inverse
+// rotary step takes back.
 //
 // Each pair of a q or k head of token t, (i, i + rot_dim/2) or (2i, 2i + 1),
 // becomes a' = a c - b s, b' = b c + a s with c, s from row positions[t] of the
