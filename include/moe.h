@@ -452,7 +452,8 @@ int moe_rope_append(const moe_append_shape_t *shape, const void *q, const void *
  *   q_stride    elements from one token's heads to the next token's, a multiple
  *               of 8 (0: adjacent)
  *   page_stride elements from page to page, a multiple of 16 (0: adjacent)
- *   scale       multiplies q . k before the softmax
+ *   scale       multiplies q . k before the softmax; finite, also times log2(e)
+ *               (and, with an E4M3 cache, times k_scale)
  *   k_scale, v_scale  static scales of an E4M3 cache (> 0, finite; ignored for bf16)
  */
 typedef struct {

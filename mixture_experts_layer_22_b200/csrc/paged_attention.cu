@@ -830,6 +830,8 @@ static int check_attn(const moe_attn_shape_t *shape)
     if (!finite(s.scale)) return MOE_ERR_INVALID_ARG;
     if (s.cache_dtype == MOE_E4M3 && !(s.k_scale > 0.0f && s.v_scale > 0.0f && finite(s.k_scale) && finite(s.v_scale)))
         return MOE_ERR_INVALID_ARG;
+    // the kernels multiply q . k, which may be 0, by this
+    if (!finite(attn_scale_log2(s))) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -252,7 +252,9 @@ BAD_ATTN = [
     (dict(page_stride=4104), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(scale=-math.inf), -1),
     (dict(cache_dtype=1, k_scale=0.0), -1), (dict(cache_dtype=1, k_scale=math.inf), -1), (dict(cache_dtype=1, v_scale=math.nan), -1),
     (dict(cache_dtype=1, v_scale=-1.0), -1), (dict(num_pages=1 << 27), -1), (dict(max_pages=1 << 27), -1), (dict(q_stride=1 << 62), -1),
-    (dict(page_stride=1 << 62), -1), (dict(num_tokens=1 << 29), -1)]
+    (dict(page_stride=1 << 62), -1), (dict(num_tokens=1 << 29), -1),
+    # times log2(e), and with codes times k_scale, beyond fp32: 0 x infinity is no score
+    (dict(scale=3e38), -1), (dict(scale=-3e38), -1), (dict(cache_dtype=1, scale=1e20, k_scale=1e20), -1)]
 
 
 @pytest.mark.parametrize("kw,code", BAD_ATTN, ids=str)
