@@ -4,29 +4,24 @@
 
 namespace moe {
 
-// A buffer: n pieces of `bytes` bytes, `step` bytes apart (a dense one is one piece).
+// A buffer: n pieces of `bytes` bytes, `step` bytes apart (a dense one is one piece), up to
+// `end`.  One that is NULL or empty ends at 0 and so shares nothing.
 struct Extent {
-    uintptr_t at;
+    uintptr_t at, end;
     int64_t bytes, step, n;
 
     Extent(const void *p, int64_t bytes_) : Extent(p, bytes_, bytes_, 1) {}
     Extent(const void *p, int64_t bytes_, int64_t step_, int64_t n_)
-        : at(reinterpret_cast<uintptr_t>(p)), bytes(bytes_), step(step_), n(n_)
+        : at(reinterpret_cast<uintptr_t>(p)), end(0), bytes(bytes_), step(step_), n(n_)
     {
-        if (step == bytes) {
-            bytes *= n;
-            n = 1;
-        }
+        if (at != 0 && bytes > 0 && n > 0) end = at + static_cast<uintptr_t>((n - 1) * step + bytes);
     }
-    bool none() const { return at == 0 || bytes <= 0 || n <= 0; }
-    uintptr_t end() const { return at + static_cast<uintptr_t>((n - 1) * step + bytes); }
 };
 
-// Exact: a piece that lies between two pieces of the other buffer shares nothing with it.
-// Only buffers that lie in one another's range are compared piece by piece.
-inline bool overlap(const Extent &a, const Extent &b)
+// Piece by piece, exactly: a piece that lies between two pieces of the other buffer shares
+// nothing with it.
+inline bool pieces_overlap(const Extent &a, const Extent &b)
 {
-    if (a.none() || b.none() || a.at >= b.end() || b.at >= a.end()) return false;
     const Extent &few = a.n <= b.n ? a : b, &many = a.n <= b.n ? b : a;
     for (int64_t i = 0; i < few.n; ++i) {
         const uintptr_t from = few.at + static_cast<uintptr_t>(i * few.step), behind = from + static_cast<uintptr_t>(few.bytes);
@@ -37,5 +32,8 @@ inline bool overlap(const Extent &a, const Extent &b)
     }
     return false;
 }
+
+// Nearly always two comparisons: a call has some fifty pairs of buffers.
+inline bool overlap(const Extent &a, const Extent &b) { return a.at < b.end && b.at < a.end && pieces_overlap(a, b); }
 
 }  // namespace moe
