@@ -475,7 +475,8 @@ int moe_attn_workspace_size(const moe_attn_shape_t *shape, size_t *bytes);
  * the accumulation are fp32; p enters its product with v in 16 bits: fp16 with an
  * E4M3 cache; with a bf16 cache bf16, and as two bf16, a high and a low part, for
  * requests with at most 16 query rows a key/value head (for all requests where
- * max_q says that there are no others).
+ * max_q says that there are no others).  The sums of p v are divided by the sum of p
+ * at the end, and p may be up to 2^8 until then: values are to stay below 2^119 / kv_len.
  *   q [num_tokens, n_heads, head_dim] bf16 (16-byte aligned), k_cache, v_cache
  *   (16-byte aligned), block_table [B, max_pages], q_start [B+1], kv_len [B] in;
  *   out [num_tokens, n_heads, head_dim] bf16 (16-byte aligned) out.

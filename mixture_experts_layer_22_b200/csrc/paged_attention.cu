@@ -9,12 +9,17 @@
 //
 // Requests with at most 16 query rows a key/value head are bound by reading the
 // cache and go to paged_decode.cu, those with more by the products and exponentials
-// and go to paged_attention_tc.cu.  The kernel here takes head_dim 256 (for both:
-// kWM = 1 and 4), whose accumulators leave the others no room, and with many rows a
-// scale that is zero or negative or a group of more than 128 heads.  It is mma.sync with 64-key
-// blocks in a ring that all four warps fill by cp.async and read behind a block
-// barrier; the warps lie down the rows, or with few rows along the keys of a block.
-// 130 to 160 TFLOP/s on prompts at head_dim 128.
+// and go to paged_attention_tc.cu.  The kernel here takes head_dim 256 for both
+// (kWM = 1 and 4): a decode warp's output alone would be 128 registers a thread, and two
+// 128-row tiles with their scores more than tensor memory's 512 columns.  With many rows
+// it also takes a scale whose log2 form is below 1e-37 (zero and negative ones with
+// it), a group of more than 128 heads and a token stride of 2^39 elements or more.  It is
+// mma.sync with 64-key blocks in a ring that all four warps fill by cp.async and
+// read behind a block barrier; the warps lie down the rows, or with few rows along the
+// keys of a block.  At head_dim 256 (32 and 8 heads): 32 requests of 8192 keys 455 us (4.7
+// TB/s) in bf16, 360 us (3.0 TB/s) in E4M3, whose codes are converted in the chain; 4 prompts
+// of 2048 tokens 1465 us (190 TFLOP/s) and 1890 us, the E4M3 form with 764 bytes spilled;
+// 1024 tokens over 8192 keys 1160 us.  mma.sync's rate bounds the many rows.
 #include <atomic>
 
 #include "overlap.cuh"

@@ -15,21 +15,25 @@
 //   - a block is worked on in two halves of 64 keys with their own columns of S:
 //     the scores of one half are made while the softmax of the other runs, so the
 //     softmax never waits for its own products;
-//   - P (bf16) takes the place of S in tensor memory and is the A operand of the
-//     second product from there: it never goes through shared memory;
+//   - P takes the place of S in tensor memory and is the A operand of the second
+//     product from there: it never goes through shared memory.  It has the type of V,
+//     as one MMA's operands must: bf16, or with codes fp16.  A second bf16 part, as
+//     decode has, would double the second product; without it the error against 64 bits is
+//     0.0021 to 0.0023 of the output's norm where the output's own rounding gives 0.0017;
 //   - O stays in tensor memory.  Its rows are rescaled only when their maximum
 //     has grown by more than 2^8 since the last time (until then p may exceed 1,
 //     which costs nothing in 16 bits and in fp32 sums);
 //   - an item's Q is loaded when the last scores of the item before are done, and
 //     its first scores are issued behind that item's last products, so that they
 //     run while its output is written.
-// Measured: 1024 tokens over 32768 keys, 32 and 8 heads of 128, bf16: 515 us, 1050
-// TFLOP/s, in a burst, 590 us in a long run, where the power limit brings the SMs
-// from 1.97 to 1.54 GHz (a library product of the same length reaches 1391); every
-// form of the softmax tried gave the burst figure within 1%: turns at the
-// exponentials, part of them as polynomials on the fp32 pipe, other orders, the next
-// scores fetched early.  4 prompts of 2048 tokens: 196 us, of which the ends of items
-// (5000 cycles each for the output) and their first blocks are a third.
+// Measured: 1024 tokens over 32768 keys, 32 and 8 heads of 128, bf16: 525 us, 1030
+// TFLOP/s, in ten replays of a graph, 605 us in a long run, where the power limit
+// brings the SMs from 1.97 to 1.54 GHz (a library product of the same length reaches
+// 1391); every form of the softmax tried gave the burst figure within 1%: turns at
+// the exponentials, part of them as polynomials on the fp32 pipe, other orders, the
+// next scores fetched early.  4 prompts of 2048 tokens: 182 and 196 us, of which the ends
+// of items (5000 cycles each for the output) and their first blocks are a third; both
+// are on the softmax warps, as O's rescaling is.
 // A tile holds whole tokens: tile_rows / 2 = group * floor(128 / group) rows.
 // Warp roles: 0-3 and 4-7 softmax of tile 0 and 1 and the output, 8 and 9 issue the
 // MMAs of tile 0 and 1 (apart, because a wait of one must not hold up the other)
@@ -831,8 +835,8 @@ static cudaError_t launch_tc(const AttnParams &p, int sms, bool chained, cudaStr
 cudaError_t launch_attn_tc(const AttnParams &p, int head_dim, bool e4m3, int sms, bool chained, cudaStream_t st)
 {
     // TMA takes a block as whole boxes: pages that divide it (8 rows at least, the
-    // swizzle's pattern), or that it divides.  Against row copies: 4 prompts of 2048
-    // tokens 223 to 249 us, a mixed batch with 16-token pages 193 to 212 us.
+    // swizzle's pattern), or that it divides.  Against row copies, in replays of a graph:
+    // 4 prompts of 2048 tokens 183 to 222 us, a mixed batch with 16-token pages 137 to 172.
     const bool boxes = ((p.page_size >= 8 && 128 % p.page_size == 0) || p.page_size % 128 == 0) && p.page_stride < 1ll << 39;
     if (head_dim == 64)
         return e4m3    ? launch_tc<64, kLoadCodes>(p, sms, chained, st)
