@@ -176,3 +176,17 @@ def _pair_norm(x, rot, il):
         n = (x[..., :rot // 2] ** 2 + x[..., rot // 2:rot] ** 2).sqrt()
         y[..., :rot // 2], y[..., rot // 2:rot] = n, n
     return y
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("power", [-100, 100, 107])
+def test_values_near_either_end_of_the_range(dim, power):
+    """Values of up to 2^(power + 2.3), 700 keys: below 2^119 / kv_len.  Times a power of two
+    everything keeps its roundings."""
+    b = ref.Batch([1, 45, 2, 1], [130, 300, 2, 700], heads=8, kv_heads=2, dim=dim, seed=27)
+    assert max(float(v.abs().max()) for v in b.v) < 2 ** 2.3
+    d = Dev(b)
+    d.v_cache = (d.v_cache.float() * 2.0 ** power).to(torch.bfloat16)
+    out = d.run().cpu().double() * 2.0 ** -power
+    want, tol = b.reference()
+    assert int(d.status[0]) == 0 and ((out - want).abs() <= tol).all()
