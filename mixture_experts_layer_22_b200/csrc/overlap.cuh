@@ -19,9 +19,17 @@ struct Extent {
 };
 
 // Piece by piece, exactly: a piece that lies between two pieces of the other buffer shares
-// nothing with it.
+// nothing with it.  With one step for both (K and V pages that alternate, millions of
+// them) piece i of a and piece j of b are apart by what j - i says.
 inline bool pieces_overlap(const Extent &a, const Extent &b)
 {
+    if (a.step == b.step && a.n > 1 && b.n > 1) {
+        // the least d = j - i with which b's piece ends behind the start of a's
+        const int64_t diff = static_cast<int64_t>(a.at - b.at), x = diff - b.bytes;
+        int64_t d = x / a.step - (x % a.step < 0 ? 1 : 0) + 1;
+        if (d < 1 - a.n) d = 1 - a.n;
+        return d < b.n && d * a.step < diff + a.bytes;
+    }
     const Extent &few = a.n <= b.n ? a : b, &many = a.n <= b.n ? b : a;
     for (int64_t i = 0; i < few.n; ++i) {
         const uintptr_t from = few.at + static_cast<uintptr_t>(i * few.step), behind = from + static_cast<uintptr_t>(few.bytes);

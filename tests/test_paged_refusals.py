@@ -3,6 +3,7 @@ buffer of the unchanged call has addresses of its own, and that call is refused 
 nothing but the missing GPU."""
 import ctypes as C
 import math
+import time
 
 import pytest
 import torch
@@ -279,3 +280,24 @@ def test_attention_refuses_each_null_misaligned_and_small(lib):
     assert lib.moe_paged_attention(None, *ATTN_AT.values(), need, None) == INVALID
     assert lib.moe_attn_workspace_size(C.byref(moe.AttnShape(**ATTN)), None) == INVALID
     assert _attention(lib, dict(num_tokens=0), ws_bytes=0, **{n: None for n in ATTN_AT}) == 0
+
+
+@pytest.mark.parametrize("gap", [0, 3])
+def test_append_checks_alternating_pages_at_once(lib, gap):
+    """K and V pages that alternate in one buffer, 16 million of each, perhaps of several
+    layers: the check does not go from page to page."""
+    page = 16 * 2 * 128
+    shape = dict(page_stride=(2 + gap) * page, num_pages=1 << 24)
+    far = {n: a << 20 for n, a in APPEND_AT.items()}
+    far["v_cache"] = far["k_cache"] + 2 * page
+    t0 = time.perf_counter()
+    for _ in range(20):
+        assert _append(lib, shape, **far) == NO_GPU
+    assert time.perf_counter() - t0 < 0.3
+    for off in (16, -16):
+        moved = {**far, "v_cache": far["v_cache"] + off}
+        assert _append(lib, shape, **moved) == (INVALID if off < 0 or gap == 0 else NO_GPU)
+    # within the first gap of K and behind its last page: only whole pages count
+    last = far["k_cache"] + 2 * (2 + gap) * page * ((1 << 24) - 1)
+    assert _append(lib, shape, **{**far, "v_cache": last + 2 * page}) == NO_GPU
+    assert _append(lib, shape, **{**far, "v_cache": last + 2 * page - 16}) == INVALID
